@@ -300,6 +300,107 @@ mhc_status mhc_backward_noalloc(const void* X, const void* F_out, const float* p
                                 mhc_stream_t stream);
 
 /*
+ * The sub-layer operators.  pre and post wrap a sub-layer F; the calls below are what a
+ * feed-forward F is made of (layer norm, up projection with an activation, down projection),
+ * forward and backward, on the activations mhc_pre writes (x_in) and mhc_post and
+ * mhc_backward take (F_out, dx_in).  They have no counterpart on the pages, which leave F
+ * open.  Same conventions as above, with activations [T, d] (or [T, K], [T, N]) of type dt
+ * and 1 <= d, K, N <= 2^30; T == 0 launches nothing in the forward calls and sets the
+ * parameter gradients to zero in the backward calls.
+ */
+
+/*
+ * mhc_layer_norm -- layer norm of every token over its d channels:
+ *   mean = sum_c x_c / d      rstd = 1 / sqrt(sum_c (x_c - mean)^2 / d + eps)
+ *   y_c  = (x_c - mean) * rstd * weight_c + bias_c
+ * Inputs : x [T,d] (dt); weight [d], bias [d] fp32, each may be NULL (1 and 0).
+ * Outputs: y [T,d] (dt); mean [T], rstd [T] fp32, which the backward needs: both given or
+ *          both NULL (MHC_ERR_NULL for one alone).
+ * Statistics are fp32; the variance is summed around the mean.
+ */
+mhc_status mhc_layer_norm(const void* x, const float* weight, const float* bias, int64_t T, int d,
+                          float eps, mhc_dtype dt, void* y, float* mean, float* rstd,
+                          mhc_stream_t stream);
+
+/*
+ * mhc_layer_norm_backward_workspace_bytes -- device workspace mhc_layer_norm_backward needs
+ * for (T, d); 0 for a shape it rejects and for T == 0.  Host-side, launches nothing.
+ */
+size_t mhc_layer_norm_backward_workspace_bytes(int64_t T, int d);
+
+/*
+ * mhc_layer_norm_backward -- the gradients of <dy, y> for mhc_layer_norm's y.  With
+ * xh = (x - mean) rstd and g = dy * weight:
+ *   dx = rstd (g - sum_c(g) / d - xh sum_c(g xh) / d)
+ *   dweight_c = sum_t dy xh       dbias_c = sum_t dy
+ * Inputs : x [T,d], dy [T,d] (dt); weight [d] as given to the forward (or NULL); mean [T]
+ *          and rstd [T] as the forward wrote them.
+ * Outputs: dx [T,d] (dt); dweight [d], dbias [d] fp32, summed over all tokens in a fixed order
+ *          (repeated calls on one device are bitwise equal).  Each may be NULL: not wanted.
+ * workspace: 256-byte aligned, at least mhc_layer_norm_backward_workspace_bytes(T, d) bytes
+ *          (MHC_ERR_WORKSPACE); may be NULL when neither dweight nor dbias is wanted.
+ */
+mhc_status mhc_layer_norm_backward(const void* x, const float* weight, const float* mean,
+                                   const float* rstd, int64_t T, int d, mhc_dtype dt,
+                                   const void* dy, void* dx, float* dweight, float* dbias,
+                                   void* workspace, size_t workspace_bytes, mhc_stream_t stream);
+
+/* Activations of mhc_linear. */
+typedef enum {
+    MHC_ACT_NONE = 0,          /* z                                                    */
+    MHC_ACT_RELU = 1,          /* max(z, 0); slope 0 at z = 0                          */
+    MHC_ACT_GELU = 2,          /* z Phi(z), Phi the normal distribution function (erf) */
+    MHC_ACT_GELU_TANH = 3,     /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2      */
+    MHC_ACT_SILU = 4           /* z / (1 + exp(-z))                                    */
+} mhc_act;
+
+/*
+ * mhc_linear_workspace_bytes -- device workspace mhc_linear needs for (T, K, N) in type dt;
+ * 0 when it needs none, and for a shape or type it rejects.  Host-side, launches nothing.
+ */
+size_t mhc_linear_workspace_bytes(int64_t T, int K, int N, mhc_dtype dt);
+
+/*
+ * mhc_linear -- a projection with its epilogue, for T tokens:
+ *   z = x W^T + bias              y = act(z) + residual
+ * Inputs : x [T,K], W [N,K] (dt); bias [N] fp32 or NULL; residual [T,N] (dt) or NULL.
+ * Outputs: y [T,N] (dt); z [T,N] (dt), the pre-activation that mhc_linear_backward needs when
+ *          act is not MHC_ACT_NONE, or NULL.
+ * Products accumulate in fp32; bias, activation and residual are applied in fp32 before the
+ * one rounding to dt.
+ * workspace: 256-byte aligned, at least mhc_linear_workspace_bytes(T, K, N, dt) bytes
+ *          (MHC_ERR_WORKSPACE); may be NULL when that is 0.
+ * Errors : MHC_ERR_UNSUPPORTED for an act that is not an mhc_act value.
+ */
+mhc_status mhc_linear(const void* x, const void* W, const float* bias, const void* residual,
+                      int64_t T, int K, int N, mhc_act act, mhc_dtype dt, void* y, void* z,
+                      void* workspace, size_t workspace_bytes, mhc_stream_t stream);
+
+/*
+ * mhc_linear_backward_workspace_bytes -- device workspace mhc_linear_backward needs for
+ * (T, K, N) in type dt; 0 for a shape or type it rejects and for T == 0.  Host-side.
+ */
+size_t mhc_linear_backward_workspace_bytes(int64_t T, int K, int N, mhc_dtype dt);
+
+/*
+ * mhc_linear_backward -- the gradients of <dy, y> for mhc_linear's y.  With dz = dy * act'(z):
+ *   dx = dz W      dW = dz^T x      dbias_n = sum_t dz      (residual's gradient is dy itself)
+ * Inputs : x [T,K], W [N,K], dy [T,N] (dt); z [T,N] (dt) as mhc_linear wrote it, ignored (may
+ *          be NULL) when act is MHC_ACT_NONE.
+ * Outputs: dx [T,K], dW [N,K] (dt), dbias [N] fp32.  Each may be NULL: not wanted; x may be NULL
+ *          without dW, W without dx.  Sums over tokens run in a fixed order (repeated calls on
+ *          one device are bitwise equal).  With bf16 storage and an activation the two products
+ *          read dz rounded to bf16; dbias sums it before that rounding.
+ * workspace: 256-byte aligned, at least mhc_linear_backward_workspace_bytes(T, K, N, dt) bytes
+ *          (MHC_ERR_WORKSPACE).
+ * Errors : MHC_ERR_UNSUPPORTED for an act that is not an mhc_act value.
+ */
+mhc_status mhc_linear_backward(const void* x, const void* W, const void* z, int64_t T, int K, int N,
+                               mhc_act act, mhc_dtype dt, const void* dy, void* dx, void* dW,
+                               float* dbias, void* workspace, size_t workspace_bytes,
+                               mhc_stream_t stream);
+
+/*
  * mhc_amax_gain -- the Amax Gain Magnitude of the composite residual maps of L consecutive
  * layers ("DeepSeek-V4/mhc" page, stability paragraph; the slavadubrov.com article's numpy
  * demo): for every token and every prefix l = 1..L of the stack,

@@ -15,6 +15,9 @@ CPU fallback -- if the library is missing the calls raise.
                  eps, t_max, H, h, dX_out, dx_in, dX, dF_out, dphi, db_pre, db_post,
                  db_res, dalpha, workspace)  -> the gradients of <dX_out, X'> + <dx_in, x_in>
     mhc_backward_noalloc(...)       -> the same, in the library's fixed scratch array
+    mhc_layer_norm(x, weight, bias, eps, y, mean, rstd), mhc_layer_norm_backward(...),
+    mhc_linear(x, W, bias, y, act, residual, z, workspace), mhc_linear_backward(...)
+                                    -> what a feed-forward sub-layer F is made of
     mhc_amax_gain(H_layers, gain)   -> per-prefix row / column gains of H_res(l) ... H_res(1)
 
 Tensors are torch CUDA tensors (contiguous; X/F_out/x_in/X_out bf16 or fp32, phi, biases
@@ -30,6 +33,10 @@ import threading
 __all__ = ["mhc_pre", "mhc_pre_with_path", "mhc_pre_hc", "mhc_pre_train", "mhc_post",
            "mhc_forward_host", "mhc_forward_host_workspace_bytes", "mhc_backward",
            "mhc_backward_workspace_bytes", "mhc_backward_noalloc", "NOALLOC_SCRATCH_BYTES",
+           "mhc_layer_norm", "mhc_layer_norm_backward", "mhc_layer_norm_backward_workspace_bytes",
+           "mhc_linear", "mhc_linear_workspace_bytes", "mhc_linear_backward",
+           "mhc_linear_backward_workspace_bytes",
+           "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU",
            "mhc_amax_gain", "mhc_pre_path_for", "mhc_pre_path_ok", "mhc_device_status",
            "mhc_debug_pre_stop_after", "mhc_debug_backward_stop_after",
            "MhcError",
@@ -42,6 +49,7 @@ _LIB_PATH = os.path.join(_HERE, "libmhc_b200.so")
 MHC_F32, MHC_BF16 = 0, 1
 NOALLOC_SCRATCH_BYTES = 32 << 20      # the fixed scratch array of mhc_backward_noalloc
 PRE_AUTO, PRE_GENERIC, PRE_CLUSTER_TC, PRE_TWO_PASS_TC = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 _STATUS = {0: "MHC_OK", 1: "MHC_ERR_NULL", 2: "MHC_ERR_SHAPE", 3: "MHC_ERR_ALIGN",
            4: "MHC_ERR_DTYPE", 5: "MHC_ERR_UNSUPPORTED", 6: "MHC_ERR_CUDA", 7: "MHC_ERR_ALIAS",
            8: "MHC_ERR_WORKSPACE"}
@@ -50,6 +58,9 @@ _STATUS = {0: "MHC_OK", 1: "MHC_ERR_NULL", 2: "MHC_ERR_SHAPE", 3: "MHC_ERR_ALIGN
 EXPORTED_SYMBOLS = ("mhc_pre", "mhc_pre_with_path", "mhc_pre_hc", "mhc_pre_train", "mhc_pre_path_for",
                     "mhc_pre_path_ok", "mhc_post", "mhc_forward_host_workspace_bytes", "mhc_forward_host",
                     "mhc_backward_workspace_bytes", "mhc_backward", "mhc_backward_noalloc",
+                    "mhc_layer_norm", "mhc_layer_norm_backward_workspace_bytes",
+                    "mhc_layer_norm_backward", "mhc_linear_workspace_bytes", "mhc_linear",
+                    "mhc_linear_backward_workspace_bytes", "mhc_linear_backward",
                     "mhc_amax_gain", "mhc_status_string",
                     "mhc_last_error", "mhc_device_status", "mhc_debug_pre_stop_after",
                     "mhc_debug_backward_stop_after")
@@ -97,6 +108,21 @@ def load_library():
         lib.mhc_backward.restype = ci
         lib.mhc_backward_noalloc.argtypes = lib.mhc_backward.argtypes[:-3] + [vp]
         lib.mhc_backward_noalloc.restype = ci
+        sz = ctypes.c_size_t
+        lib.mhc_layer_norm.argtypes = [vp, fp, fp, i64, ci, cf, ci, vp, fp, fp, vp]
+        lib.mhc_layer_norm.restype = ci
+        lib.mhc_layer_norm_backward_workspace_bytes.argtypes = [i64, ci]
+        lib.mhc_layer_norm_backward_workspace_bytes.restype = sz
+        lib.mhc_layer_norm_backward.argtypes = [vp, fp, fp, fp, i64, ci, ci, vp, vp, fp, fp, vp, sz, vp]
+        lib.mhc_layer_norm_backward.restype = ci
+        lib.mhc_linear_workspace_bytes.argtypes = [i64, ci, ci, ci]
+        lib.mhc_linear_workspace_bytes.restype = sz
+        lib.mhc_linear.argtypes = [vp, vp, fp, vp, i64, ci, ci, ci, ci, vp, vp, vp, sz, vp]
+        lib.mhc_linear.restype = ci
+        lib.mhc_linear_backward_workspace_bytes.argtypes = [i64, ci, ci, ci]
+        lib.mhc_linear_backward_workspace_bytes.restype = sz
+        lib.mhc_linear_backward.argtypes = [vp, vp, vp, i64, ci, ci, ci, ci, vp, vp, vp, fp, vp, sz, vp]
+        lib.mhc_linear_backward.restype = ci
         lib.mhc_amax_gain.argtypes = [fp, ci, i64, ci, fp, vp]
         lib.mhc_amax_gain.restype = ci
         lib.mhc_pre_path_for.argtypes = [i64, ci, ci, ci]
@@ -422,6 +448,157 @@ def mhc_backward_noalloc(X, F_out, phi, b_pre, b_post, b_res, alpha_pre, alpha_p
                                       p["dF_out"], q["dphi"], q["db_pre"], q["db_post"],
                                       q["db_res"], q["dalpha"], _stream(stream, dev))
     _check(st, "mhc_backward_noalloc")
+
+
+def _shape(where, name, t, shape):
+    """A tensor argument of the sub-layer operators has exactly this shape (None passes): the C
+    ABI sees only pointers, so a smaller tensor would be read or written past its end."""
+    import torch
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{where}: {name} must be a torch tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _rows(where, name, t):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{where}: {name} must be a torch tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{where}: {name} must be two-dimensional, has shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _workspace(workspace, dev):
+    """(pointer, bytes) of an optional workspace tensor."""
+    if workspace is None:
+        return 0, 0
+    return _ptr(workspace, "workspace", device=dev), workspace.numel() * workspace.element_size()
+
+
+def mhc_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
+    """Layer norm of every token over its channels, y = (x - mean) rstd * weight + bias.
+
+    x [T, d] (bf16/fp32); weight and bias [d] fp32, either may be None (1 and 0); written in
+    place: y [T, d] (x's dtype) and, for training, mean and rstd [T] fp32 (both or neither)."""
+    import torch
+    where = "mhc_layer_norm"
+    T, d = _rows(where, "x", x)
+    for name, t, shape in (("weight", weight, (d,)), ("bias", bias, (d,)), ("y", y, (T, d)),
+                           ("mean", mean, (T,)), ("rstd", rstd, (T,))):
+        _shape(where, name, t, shape)
+    dev, f32 = x.device, torch.float32
+    dt = _dt(x)
+    px, py = _ptr(x, "x", device=dev), _ptr(y, "y", x.dtype, dev)
+    q = [_ptr(t, name, f32, dev) for name, t in (("weight", weight), ("bias", bias), ("mean", mean), ("rstd", rstd))]
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.mhc_layer_norm(px, q[0], q[1], T, d, float(eps), dt, py, q[2], q[3], _stream(stream, dev))
+    _check(st, where)
+
+
+def mhc_layer_norm_backward_workspace_bytes(T: int, d: int) -> int:
+    """Bytes of device workspace mhc_layer_norm_backward needs (0 for T = 0 and rejected shapes)."""
+    return int(load_library().mhc_layer_norm_backward_workspace_bytes(int(T), int(d)))
+
+
+def mhc_layer_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, workspace=None, stream=None):
+    """Gradients of <dy, y> for mhc_layer_norm, written in place: dx [T, d] (x's dtype), dweight
+    and dbias [d] fp32; each may be None (not wanted).  mean and rstd [T] as mhc_layer_norm wrote
+    them.  workspace: a CUDA tensor of mhc_layer_norm_backward_workspace_bytes(T, d) bytes; None
+    will do when neither dweight nor dbias is wanted."""
+    import torch
+    where = "mhc_layer_norm_backward"
+    T, d = _rows(where, "x", x)
+    for name, t, shape in (("weight", weight, (d,)), ("mean", mean, (T,)), ("rstd", rstd, (T,)), ("dy", dy, (T, d)),
+                           ("dx", dx, (T, d)), ("dweight", dweight, (d,)), ("dbias", dbias, (d,))):
+        _shape(where, name, t, shape)
+    dev, f32 = x.device, torch.float32
+    dt = _dt(x)
+    p = [_ptr(t, name, x.dtype, dev) for name, t in (("x", x), ("dy", dy), ("dx", dx))]
+    q = [_ptr(t, name, f32, dev) for name, t in (("weight", weight), ("mean", mean), ("rstd", rstd),
+                                                 ("dweight", dweight), ("dbias", dbias))]
+    ws, nbytes = _workspace(workspace, dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.mhc_layer_norm_backward(p[0], q[0], q[1], q[2], T, d, dt, p[1], p[2], q[3], q[4], ws, nbytes,
+                                         _stream(stream, dev))
+    _check(st, where)
+
+
+def _dt_of(dtype) -> int:
+    import torch
+    if isinstance(dtype, int):
+        return dtype
+    if dtype == torch.bfloat16:
+        return MHC_BF16
+    if dtype == torch.float32:
+        return MHC_F32
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def mhc_linear_workspace_bytes(T: int, K: int, N: int, dtype) -> int:
+    """Bytes of device workspace mhc_linear needs for x [T, K] and W [N, K] (0: none)."""
+    return int(load_library().mhc_linear_workspace_bytes(int(T), int(K), int(N), _dt_of(dtype)))
+
+
+def mhc_linear(x, W, bias, y, act: int = ACT_NONE, residual=None, z=None, workspace=None, stream=None):
+    """y = act(z) + residual with z = x W^T + bias, written in place.
+
+    x [T, K], W [N, K], y [T, N] and the optional residual and z [T, N] share one dtype
+    (bf16/fp32); bias [N] fp32 or None; act is one of ACT_NONE, ACT_RELU, ACT_GELU,
+    ACT_GELU_TANH, ACT_SILU.  z, when given, is written: mhc_linear_backward needs it if there is
+    an activation.  workspace: a CUDA tensor of mhc_linear_workspace_bytes(T, K, N, dtype) bytes;
+    None will do when that is 0."""
+    import torch
+    where = "mhc_linear"
+    T, K = _rows(where, "x", x)
+    N = _rows(where, "W", W)[0]
+    for name, t, shape in (("W", W, (N, K)), ("bias", bias, (N,)), ("y", y, (T, N)), ("residual", residual, (T, N)),
+                           ("z", z, (T, N))):
+        _shape(where, name, t, shape)
+    dev = x.device
+    dt = _dt(x)
+    p = [_ptr(t, name, x.dtype, dev) for name, t in (("x", x), ("W", W), ("residual", residual), ("y", y), ("z", z))]
+    pb = _ptr(bias, "bias", torch.float32, dev)
+    ws, nbytes = _workspace(workspace, dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.mhc_linear(p[0], p[1], pb, p[2], T, K, N, int(act), dt, p[3], p[4], ws, nbytes,
+                            _stream(stream, dev))
+    _check(st, where)
+
+
+def mhc_linear_backward_workspace_bytes(T: int, K: int, N: int, dtype) -> int:
+    """Bytes of device workspace mhc_linear_backward needs for x [T, K] and W [N, K]."""
+    return int(load_library().mhc_linear_backward_workspace_bytes(int(T), int(K), int(N), _dt_of(dtype)))
+
+
+def mhc_linear_backward(x, W, z, dy, dx, dW, dbias, workspace, act: int = ACT_NONE, stream=None):
+    """Gradients of <dy, y> for mhc_linear, written in place: with dz = dy * act'(z),
+    dx = dz W [T, K] and dW = dz^T x [N, K] (x's dtype), dbias = sum_t dz [N] fp32; each may be
+    None (not wanted).  The residual's gradient is dy.  z [T, N] as mhc_linear wrote it; None will
+    do for ACT_NONE.  workspace: a CUDA tensor of mhc_linear_backward_workspace_bytes(T, K, N,
+    dtype) bytes."""
+    import torch
+    where = "mhc_linear_backward"
+    T, K = _rows(where, "x", x)
+    N = _rows(where, "W", W)[0]
+    for name, t, shape in (("W", W, (N, K)), ("z", z, (T, N)), ("dy", dy, (T, N)), ("dx", dx, (T, K)),
+                           ("dW", dW, (N, K)), ("dbias", dbias, (N,))):
+        _shape(where, name, t, shape)
+    dev = x.device
+    dt = _dt(x)
+    p = [_ptr(t, name, x.dtype, dev) for name, t in (("x", x), ("W", W), ("z", z), ("dy", dy), ("dx", dx), ("dW", dW))]
+    pb = _ptr(dbias, "dbias", torch.float32, dev)
+    ws, nbytes = _workspace(workspace, dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.mhc_linear_backward(p[0], p[1], p[2], T, K, N, int(act), dt, p[3], p[4], p[5], pb, ws, nbytes,
+                                     _stream(stream, dev))
+    _check(st, where)
 
 
 def mhc_amax_gain(H_layers, gain, stream=None):

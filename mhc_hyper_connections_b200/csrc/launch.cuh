@@ -152,6 +152,74 @@ cudaError_t bwd_tc_status(unsigned* out, bool clear);
 // per CTA (< 0: never) and give up a wait after `wait_ns`.
 void bwd_tc_set_stop(int stop_stage, unsigned long long wait_ns);
 
+// Layer norm over the channels of a token (layer_norm.cu), forward and backward.
+struct LnArgs {
+    const void* x;
+    const float* w;              // null: 1
+    const float* b;              // null: 0 (forward)
+    int64_t T;
+    int d;
+    float eps;
+    DType dt;
+    void* y;
+    float* mean;                 // forward: written (or both null); backward: read
+    float* rstd;
+    const void* dy;
+    void* dx;                    // null: not wanted
+    float* dw;                   // null: not wanted
+    float* db;
+    float* part;                 // layer_norm_part_floats floats; null when neither dw nor db is wanted
+    cudaStream_t stream;
+};
+int64_t layer_norm_part_floats(int64_t T, int d);
+cudaError_t launch_layer_norm(const LnArgs& a);
+cudaError_t launch_layer_norm_backward(const LnArgs& a);
+
+// The linear product with its epilogue, forward and backward (linear.cu).
+enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+struct LinearArgs {
+    const void* x;               // [T, K]
+    const void* W;               // [N, K]
+    const float* bias;           // [N] or null
+    const void* residual;        // [T, N] or null
+    int64_t T;
+    int K, N;
+    Act act;
+    DType dt;
+    void* y;                     // [T, N]
+    void* z;                     // forward: [T, N] or null, written; backward: read
+    const void* dy;
+    void* dx;                    // null: not wanted
+    void* dW;
+    float* dbias;
+    void* workspace;
+    cudaStream_t stream;
+};
+size_t linear_workspace(int64_t T, int K, int N, DType dt);
+size_t linear_backward_workspace(int64_t T, int K, int N, DType dt);
+cudaError_t launch_linear(const LinearArgs& a);
+cudaError_t launch_linear_backward(const LinearArgs& a);
+
+// One product D[m][n] = sum_k A(m, k) B(n, k) with the epilogue of mhc_linear; A(m, k) lies at
+// A + m lda + k, or at A + k lda + m where a_mn is set, and B likewise.  D, z and residual are
+// [M, N] with N-element rows.
+struct GemmArgs {
+    const void* A;
+    const void* B;
+    int64_t lda, ldb;
+    bool a_mn, b_mn;
+    int64_t M, N, K;
+    const float* bias;           // [N] or null
+    const void* residual;
+    Act act;
+    void* D;
+    void* z;
+    DType dt;
+    cudaStream_t stream;
+};
+cudaError_t launch_gemm_generic(const GemmArgs& a);
+
 // Amax Gain Magnitude of composite residual maps (diagnostics.cu).
 cudaError_t launch_amax_gain(const float* Hs, int L, int64_t T, int n, float* gain, cudaStream_t s);
 cudaError_t launch_backward(const BwdArgs& a);
