@@ -421,7 +421,8 @@ mhc_status mhc_amax_gain(const float* H_layers, int L, int64_t T, int n, float* 
  * kernels.  Their waits between warps and between the CTAs of a cluster are bounded in
  * time (1 s each); a wait that expires makes the kernel stop early, leaving its outputs
  * incomplete, and sets a bit here naming the wait: bits 0-15 the cluster pre kernel, 16-23
- * the two-pass pre kernels, 24-31 the tensor-core dX / dphi step of mhc_backward.  *code = 0
+ * the two-pass pre kernels, 24-28 the tensor-core dX / dphi step of mhc_backward, 29-31 the
+ * tensor-core products of mhc_linear and mhc_linear_backward.  *code = 0
  * means every wait of every launch since the last read completed.  Blocks until prior work on the legacy default
  * stream (and streams that synchronise with it) has finished.  No counterpart on the
  * pages: this is the library's failure report.
@@ -449,7 +450,7 @@ mhc_status mhc_debug_pre_stop_after(int32_t tiles, uint32_t wait_limit_us);
  * up a wait after `wait_limit_us` microseconds (default 1000000; accepted range 1000 ..
  * 10000000, else MHC_ERR_SHAPE).  Every stage before the stop completes (its dX tile is
  * stored); the waits for the stage never loaded run into their limit, the step sets bits
- * 24-31 in mhc_device_status, lets its copies and MMAs in flight complete and returns with dX
+ * 24-28 in mhc_device_status, lets its copies and MMAs in flight complete and returns with dX
  * and the parameter gradients incomplete.  Process-wide, from the next launch.  No
  * counterpart on the pages: a library test facility for the bounded waits.
  */

@@ -639,7 +639,7 @@ def mhc_debug_pre_stop_after(tiles: int, wait_limit_us: int = 1_000_000) -> None
 def mhc_debug_backward_stop_after(stages: int, wait_limit_us: int = 1_000_000) -> None:
     """Test hook of the backward's tensor-core dX / dphi step: later launches stop loading
     after `stages` 64-token stages per CTA (stages < 0 restores normal operation) and give up
-    a wait after `wait_limit_us` microseconds; mhc_device_status() then reports bits 24-31."""
+    a wait after `wait_limit_us` microseconds; mhc_device_status() then reports bits 24-28."""
     _check(load_library().mhc_debug_backward_stop_after(int(stages), int(wait_limit_us)),
            "mhc_debug_backward_stop_after")
 

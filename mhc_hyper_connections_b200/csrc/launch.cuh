@@ -219,6 +219,11 @@ struct GemmArgs {
     cudaStream_t stream;
 };
 cudaError_t launch_gemm_generic(const GemmArgs& a);
+// The same on the tensor cores (linear_tc.cu), for products gemm_tc_ok accepts: bf16 operands whose
+// rows are 16-byte aligned.
+bool gemm_tc_ok(const GemmArgs& a);
+cudaError_t launch_gemm_tc(const GemmArgs& a);
+cudaError_t linear_tc_status(unsigned* out, bool clear);
 
 // Amax Gain Magnitude of composite residual maps (diagnostics.cu).
 cudaError_t launch_amax_gain(const float* Hs, int L, int64_t T, int n, float* gain, cudaStream_t s);

@@ -126,6 +126,8 @@ cudaError_t launch_dz(const LinearArgs& a, void* dz, int64_t ld, float* part) {
     return e;
 }
 
+cudaError_t product(const GemmArgs& g) { return gemm_tc_ok(g) ? launch_gemm_tc(g) : launch_gemm_generic(g); }
+
 // regions of the backward's workspace, in bytes
 struct BackwardLayout {
     size_t dz, part, total;
@@ -159,7 +161,7 @@ cudaError_t launch_linear(const LinearArgs& a) {
     g.M = a.T; g.N = a.N; g.K = a.K;
     g.bias = a.bias; g.residual = a.residual; g.act = a.act; g.D = a.y; g.z = a.z;
     g.dt = a.dt; g.stream = a.stream;
-    return launch_gemm_generic(g);
+    return product(g);
 }
 
 cudaError_t launch_linear_backward(const LinearArgs& a) {
@@ -182,14 +184,14 @@ cudaError_t launch_linear_backward(const LinearArgs& a) {
         g.B = a.W; g.ldb = a.K;
         g.M = a.T; g.N = a.K; g.K = a.N;
         g.D = a.dx;
-        e = launch_gemm_generic(g);
+        e = product(g);
     }
     if (e == cudaSuccess && a.dW) {          // dW[n][k] = sum_t dz[t][n] x[t][k]
         g.a_mn = true;
         g.B = a.x; g.ldb = a.K;
         g.M = a.N; g.N = a.K; g.K = a.T;
         g.D = a.dW;
-        e = launch_gemm_generic(g);
+        e = product(g);
     }
     return e;
 }

@@ -18,7 +18,11 @@ ACT = {a: getattr(mhc, "ACT_" + a.upper()) for a in ACTS}
 SHAPES = [(1, 1, 1), (1, 64, 64), (1, 4096, 1024), (1, 129, 37), (2, 8, 8), (3, 17, 5), (7, 64, 257), (8, 512, 136),
           (16, 1024, 512), (17, 96, 128), (33, 72, 200), (48, 2048, 520), (64, 256, 1024), (65, 130, 66),
           (100, 1027, 130), (127, 128, 127), (128, 64, 128), (129, 192, 257), (200, 320, 96), (255, 65, 511),
-          (256, 256, 256), (300, 100, 300), (513, 1031, 264), (777, 264, 1029), (1024, 512, 768), (2100, 136, 520)]
+          (256, 256, 256), (300, 100, 300), (513, 1031, 264), (777, 264, 1029), (1024, 512, 768), (2100, 136, 520),
+          # enough 256-wide tiles for the paired kernel: forward, dx and dW in turn, several tiles per
+          # pair, ragged in each direction, rows of outputs that are not 16-byte aligned
+          (2500, 200, 2100), (2311, 72, 2565), (5000, 64, 5000), (2500, 2100, 200), (3001, 2056, 168), (100, 2504, 2104),
+          (520, 4104, 3336)]
 
 
 def _case(T, K, N, dt, seed=0):
