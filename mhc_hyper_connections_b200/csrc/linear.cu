@@ -29,43 +29,67 @@ int64_t dz_runs(int64_t T, int N) {
     return std::min(want, (T + DZ_ROWS - 1) / DZ_ROWS);
 }
 
-// VEC columns per thread; dz null: column sums only; part null: no sums
-template <typename T, int VEC>
+// A thread takes VEC columns and four tokens at a time (their loads are in flight together).  dz
+// null: column sums only; part null: no sums.
+template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(DZ_COLS* DZ_ROWS)
-dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, int64_t run, int act,
-          T* __restrict__ dz, int64_t ld, float* __restrict__ part) {
+dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, int64_t run, T* __restrict__ dz,
+          int64_t ld, float* __restrict__ part) {
+    constexpr int U = 4;
     __shared__ float sm[DZ_ROWS][DZ_COLS * VEC + 1];
     const int tx = threadIdx.x % DZ_COLS, ty = threadIdx.x / DZ_COLS;
     const int64_t c = ((int64_t)blockIdx.x * DZ_COLS + tx) * VEC;
     const int64_t t0 = (int64_t)blockIdx.y * run, t1 = t0 + run < Tn ? t0 + run : Tn;
     float s[VEC] = {};
     if (c < N) {
-        for (int64_t t = t0 + ty; t < t1; t += DZ_ROWS) {
-            float g[VEC];
+        for (int64_t t = t0 + ty; t < t1; t += DZ_ROWS * U) {
+            float g[U][VEC], zf[U][VEC];
             if constexpr (VEC > 1) {
-                Vec16<T>::unpack(ld_stream_v4(dy + t * N + c), g);
+                uint4 rg[U], rz[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t tu = t + u * DZ_ROWS;
+                    rg[u] = rz[u] = make_uint4(0, 0, 0, 0);
+                    if (tu < t1) {
+                        rg[u] = ld_stream_v4(dy + tu * N + c);
+                        if constexpr (ACT != ACT_NONE) rz[u] = ld_stream_v4(z + tu * N + c);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    Vec16<T>::unpack(rg[u], g[u]);
+                    Vec16<T>::unpack(rz[u], zf[u]);
+                }
             } else {
-                g[0] = to_f32(__ldg(dy + t * N + c));
-            }
-            if (z) {
-                float zf[VEC];
-                if constexpr (VEC > 1) {
-                    Vec16<T>::unpack(ld_stream_v4(z + t * N + c), zf);
-                } else {
-                    zf[0] = to_f32(__ldg(z + t * N + c));
-                }
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) g[e] *= act_slope(zf[e], act);
-            }
-            if (dz) {
-                if constexpr (VEC > 1) {
-                    st_v4(dz + t * ld + c, Vec16<T>::pack(g));
-                } else {
-                    store_elem(dz + t * ld + c, g[0]);
+                for (int u = 0; u < U; ++u) {
+                    const int64_t tu = t + u * DZ_ROWS;
+                    g[u][0] = zf[u][0] = 0.f;
+                    if (tu < t1) {
+                        g[u][0] = to_f32(__ldg(dy + tu * N + c));
+                        if constexpr (ACT != ACT_NONE) zf[u][0] = to_f32(__ldg(z + tu * N + c));
+                    }
                 }
             }
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s[e] += g[e];
+            for (int u = 0; u < U; ++u) {
+                const int64_t tu = t + u * DZ_ROWS;
+                if (tu >= t1) break;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    // rounded as a product whether or not dz is stored, so that the sums are the same bits
+                    if constexpr (ACT != ACT_NONE)
+                        g[u][e] = __fmul_rn(g[u][e], act_slope<ACT, sizeof(T) == 2>(zf[u][e]));
+                    s[e] += g[u][e];
+                }
+                if (dz) {
+                    if constexpr (VEC > 1) {
+                        st_v4(dz + tu * ld + c, Vec16<T>::pack(g[u]));
+                    } else {
+                        store_elem(dz + tu * ld + c, g[u][0]);
+                    }
+                }
+            }
         }
     }
     if (!part) return;
@@ -101,6 +125,23 @@ sum_rows_kernel(const float* __restrict__ part, int64_t P, int N, float* __restr
     }
 }
 
+template <typename T, int VEC>
+void start_dz(const LinearArgs& a, void* dz, int64_t ld, int64_t run, int64_t rows, float* sums) {
+    const int cols = DZ_COLS * VEC;
+    const dim3 grid((unsigned)((a.N + (int64_t)cols - 1) / cols), (unsigned)rows);
+    auto go = [&](auto kern) {
+        kern<<<grid, DZ_COLS * DZ_ROWS, 0, a.stream>>>(static_cast<const T*>(a.dy), static_cast<const T*>(a.z), a.T,
+                                                       a.N, run, static_cast<T*>(dz), ld, sums);
+    };
+    switch (a.act) {
+        case ACT_RELU: go(dz_kernel<T, VEC, ACT_RELU>); break;
+        case ACT_GELU: go(dz_kernel<T, VEC, ACT_GELU>); break;
+        case ACT_GELU_TANH: go(dz_kernel<T, VEC, ACT_GELU_TANH>); break;
+        case ACT_SILU: go(dz_kernel<T, VEC, ACT_SILU>); break;
+        default: go(dz_kernel<T, VEC, ACT_NONE>); break;
+    }
+}
+
 template <typename T>
 cudaError_t launch_dz(const LinearArgs& a, void* dz, int64_t ld, float* part) {
     constexpr int V = Vec16<T>::VEC;
@@ -108,17 +149,10 @@ cudaError_t launch_dz(const LinearArgs& a, void* dz, int64_t ld, float* part) {
     const int64_t run = ((a.T + runs - 1) / runs + DZ_ROWS - 1) / DZ_ROWS * DZ_ROWS;
     const int64_t rows = (a.T + run - 1) / run;      // runs that hold tokens
     float* sums = a.dbias ? (rows == 1 ? a.dbias : part) : nullptr;
-    const bool vec = a.N % V == 0 && ld % V == 0 && (uintptr_t)a.dy % 16 == 0 && (uintptr_t)a.z % 16 == 0;
-    const int cols = DZ_COLS * (vec ? V : 1);
-    const dim3 grid((unsigned)((a.N + (int64_t)cols - 1) / cols), (unsigned)rows);
-    const T* z = a.act == ACT_NONE ? nullptr : static_cast<const T*>(a.z);
-    if (vec) {
-        dz_kernel<T, V><<<grid, DZ_COLS * DZ_ROWS, 0, a.stream>>>(static_cast<const T*>(a.dy), z, a.T, a.N, run,
-                                                                (int)a.act, static_cast<T*>(dz), ld, sums);
-    } else {
-        dz_kernel<T, 1><<<grid, DZ_COLS * DZ_ROWS, 0, a.stream>>>(static_cast<const T*>(a.dy), z, a.T, a.N, run,
-                                                                (int)a.act, static_cast<T*>(dz), ld, sums);
-    }
+    if (a.N % V == 0 && ld % V == 0 && (uintptr_t)a.dy % 16 == 0 && (uintptr_t)a.z % 16 == 0)
+        start_dz<T, V>(a, dz, ld, run, rows, sums);
+    else
+        start_dz<T, 1>(a, dz, ld, run, rows, sums);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.dbias && rows > 1)
         e = launch_pdl(sum_rows_kernel, dim3((unsigned)((a.N + (int64_t)31) / 32)), dim3(256), 0, a.stream, part,

@@ -78,21 +78,23 @@ gemm_kernel(const T* __restrict__ A, const T* __restrict__ B, int64_t lda, int64
         }
         __syncthreads();
     }
+    with_act(act, [&](auto kind) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t m = m0 + 16 * (i & ~3) + 4 * ty + (i & 3);
-        if (m >= M) continue;
+        for (int i = 0; i < TM; ++i) {
+            const int64_t m = m0 + 16 * (i & ~3) + 4 * ty + (i & 3);
+            if (m >= M) continue;
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const int64_t n = n0 + 16 * (j & ~3) + 4 * tx + (j & 3);
-            if (n >= N) continue;
-            const float v = acc[i][j] + (bias ? __ldg(bias + n) : 0.f);
-            if (z) store_elem(z + m * N + n, v);
-            float o = act_value(v, act);
-            if (residual) o += to_f32(__ldg(residual + m * N + n));
-            store_elem(D + m * N + n, o);
+            for (int j = 0; j < TM; ++j) {
+                const int64_t n = n0 + 16 * (j & ~3) + 4 * tx + (j & 3);
+                if (n >= N) continue;
+                const float v = acc[i][j] + (bias ? __ldg(bias + n) : 0.f);
+                if (z) store_elem(z + m * N + n, v);
+                float o = act_value<kind(), sizeof(T) == 2>(v);
+                if (residual) o += to_f32(__ldg(residual + m * N + n));
+                store_elem(D + m * N + n, o);
+            }
         }
-    }
+    });
 }
 
 template <typename T, int TM, bool A_MN, bool B_MN>

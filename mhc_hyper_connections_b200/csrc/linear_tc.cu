@@ -334,10 +334,10 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
                     for (int j = 0; j < 64; ++j) v[j] += c0 + j < N ? __ldg(ep.bias + c0 + j) : 0.f;
                 }
                 if (ep.z) put(ep.z);
-                if (ep.act != ACT_NONE) {
+                with_act(ep.act, [&](auto kind) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = act_value(v[j], ep.act);
-                }
+                    for (int j = 0; j < 64; ++j) v[j] = act_value<kind(), true>(v[j]);
+                });
                 if (ep.residual) {
                     if (ep.vec) {
 #pragma unroll
@@ -486,14 +486,24 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
     const int64_t r = (int64_t)m0 + 32 * q + lane;
     const uint32_t tq = tm + ((uint32_t)(32 * q) << 16);
     const float bias = warp >= 2 && ep.bias && r < Mr ? __ldg(ep.bias + r) : 0.f;
-    auto emit = [&](int c, float v) {
-        if (r >= Mr || n0 + c >= Nc) return;
-        const int64_t at = (n0 + (int64_t)c) * Mr + r;
-        v += bias;
-        if (ep.z) store_elem(ep.z + at, v);
-        v = act_value(v, ep.act);
-        if (ep.residual) v += to_f32(__ldg(ep.residual + at));
-        store_elem(ep.D + at, v);
+    // the outputs of columns c .. c + n - 1 (n <= 16) from their sums
+    auto emit = [&](int c, int n, float (&v)[16]) {
+        if (r >= Mr) return;
+        if (ep.z) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j < n && n0 + c + j < Nc) store_elem(ep.z + (n0 + (int64_t)c + j) * Mr + r, v[j] + bias);
+        }
+        with_act(ep.act, [&](auto kind) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j < n && n0 + c + j < Nc) {
+                    const int64_t at = (n0 + (int64_t)c + j) * Mr + r;
+                    float o = act_value<kind(), true>(v[j] + bias);
+                    if (ep.residual) o += to_f32(__ldg(ep.residual + at));
+                    store_elem(ep.D + at, o);
+                }
+        });
     };
     constexpr int HALF = BN / 2, STEP = HALF < 16 ? HALF : 16;      // columns of a warp, and per TMEM load
     if (S == 1) {
@@ -509,8 +519,7 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
                     v[3] = __uint_as_float(lo.w); v[4] = __uint_as_float(hi.x); v[5] = __uint_as_float(hi.y);
                     v[6] = __uint_as_float(hi.z); v[7] = __uint_as_float(hi.w);
                 }
-#pragma unroll
-                for (int j = 0; j < STEP; ++j) emit(c + j, v[j]);
+                emit(c, STEP, v);
             }
         }
     } else {
@@ -534,12 +543,20 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
         __syncwarp();
         cluster_sync_all();
         if (warp >= 2 && done) {
-            const int per = BN / S;
-            for (int c = rank * per + h; c < (rank + 1) * per; c += 2) {
-                const uint32_t at = smem_u32(part + c * 128 + 32 * q + lane);
-                float v = 0.f;
-                for (int p = 0; p < S; ++p) v += ld_cluster_f32(mapa(at, (uint32_t)p));
-                emit(c, v);
+            // this CTA's BN / S columns, half of them per warp of a lane quarter
+            const int per = BN / S / 2, c_lo = rank * 2 * per + h * per;
+            for (int c = c_lo; c < c_lo + per; c += 16) {
+                const int n = per < 16 ? per : 16;
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                for (int p = 0; p < S; ++p) {
+                    const uint32_t at = mapa(smem_u32(part + c * 128 + 32 * q + lane), (uint32_t)p);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < n) v[j] += ld_cluster_f32(at + j * 512);
+                }
+                emit(c, n, v);
             }
         }
         __syncwarp();

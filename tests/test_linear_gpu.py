@@ -60,9 +60,10 @@ def _fwd_check(c, act, got, bias=True, residual=True):
         s = s + c["bias"].double().abs()
     y = act64(z, act)
     # the activation's slope is at most 1.13 in size, and its own fp32 evaluation is off by at most
-    # 8 u |z| (a few roundings and the library function's two)
+    # 8 u |z| (a few roundings and the library function's two), or by 2^-16 |y| in its short form for
+    # bf16 storage
     tz = sum_tol(x.shape[1]) * s
-    ty = 1.13 * tz + 8 * U * z.abs()
+    ty = 1.13 * tz + 8 * U * z.abs() + (2.0 ** -16 * y.abs() if dt == BF and act != "none" else 0)
     if residual:
         y = y + c["residual"].double()
         ty = ty + 2 * U * (c["residual"].double().abs() + z.abs())
@@ -86,9 +87,9 @@ def _bwd_check(c, z, act, got):
     x, W, dy, dt = c["x"].double(), c["W"].double(), c["dy"].double(), c["x"].dtype
     T, N = dy.shape
     dz = dy if act == "none" else dy * slope64(z.double(), act)
-    # dz: the slope's fp32 evaluation (16 u of 1.13 + |z| phi(z) terms below 2) and one rounding to
-    # the storage type as the products' operand
-    e0 = torch.zeros_like(dz) if act == "none" else 32 * U * dy.abs()
+    # dz: the slope's fp32 evaluation (16 u of 1.13 + |z| phi(z) terms below 2; 2^-16 in its short form
+    # for bf16 storage) and one rounding to the storage type as the products' operand
+    e0 = torch.zeros_like(dz) if act == "none" else (32 * U if dt == F32 else 2.0 ** -16) * dy.abs()
     e = e0 if act == "none" or dt == F32 else e0 + half(dt) * dz.abs()
     dx, dW, db = dz @ W, dz.T @ x, dz.sum(0)
     check(got[0], dx, half(dt) * dx.abs() + e @ W.abs() + sum_tol(N) * (dz.abs() @ W.abs()), "dx")
