@@ -450,18 +450,6 @@ def mhc_backward_noalloc(X, F_out, phi, b_pre, b_post, b_res, alpha_pre, alpha_p
     _check(st, "mhc_backward_noalloc")
 
 
-def _shape(where, name, t, shape):
-    """A tensor argument of the sub-layer operators has exactly this shape (None passes): the C
-    ABI sees only pointers, so a smaller tensor would be read or written past its end."""
-    import torch
-    if t is None:
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{where}: {name} must be a torch tensor")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {shape}")
-
-
 def _rows(where, name, t):
     import torch
     if not isinstance(t, torch.Tensor):
@@ -471,11 +459,50 @@ def _rows(where, name, t):
     return t.shape
 
 
+def _pointers(where, dev, specs):
+    """Device pointers of tensor arguments given as (name, tensor or None, shape, dtype).  Every shape
+    is checked first (the C ABI sees only pointers, so a smaller tensor would be read or written past
+    its end), then device, dtype and contiguity."""
+    import torch
+    for name, t, shape, _ in specs:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{where}: {name} must be a torch tensor")
+        if t.shape != shape:
+            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    out = []
+    for name, t, _, dtype in specs:
+        if t is None:
+            out.append(0)
+        elif t.dtype == dtype and t.device == dev and t.is_cuda and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            out.append(_ptr(t, name, dtype, dev))      # raises, naming the tensor
+    return out
+
+
 def _workspace(workspace, dev):
     """(pointer, bytes) of an optional workspace tensor."""
     if workspace is None:
         return 0, 0
     return _ptr(workspace, "workspace", device=dev), workspace.numel() * workspace.element_size()
+
+
+def _call(where, fn, dev, stream, args):
+    """fn(*args, stream) with `dev` current, on the given or the current stream."""
+    import torch
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev.index)      # current_stream() without its object
+    else:
+        s = _stream(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st:
+        _check(st, where)
 
 
 def mhc_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
@@ -486,17 +513,11 @@ def mhc_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
     import torch
     where = "mhc_layer_norm"
     T, d = _rows(where, "x", x)
-    for name, t, shape in (("weight", weight, (d,)), ("bias", bias, (d,)), ("y", y, (T, d)),
-                           ("mean", mean, (T,)), ("rstd", rstd, (T,))):
-        _shape(where, name, t, shape)
-    dev, f32 = x.device, torch.float32
-    dt = _dt(x)
-    px, py = _ptr(x, "x", device=dev), _ptr(y, "y", x.dtype, dev)
-    q = [_ptr(t, name, f32, dev) for name, t in (("weight", weight), ("bias", bias), ("mean", mean), ("rstd", rstd))]
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.mhc_layer_norm(px, q[0], q[1], T, d, float(eps), dt, py, q[2], q[3], _stream(stream, dev))
-    _check(st, where)
+    dt, xt, f32, dev = _dt(x), x.dtype, torch.float32, x.device
+    px, pw, pb, py, pm, pr = _pointers(where, dev, (
+        ("x", x, x.shape, xt), ("weight", weight, (d,), f32), ("bias", bias, (d,), f32), ("y", y, x.shape, xt),
+        ("mean", mean, (T,), f32), ("rstd", rstd, (T,), f32)))
+    _call(where, load_library().mhc_layer_norm, dev, stream, (px, pw, pb, T, d, float(eps), dt, py, pm, pr))
 
 
 def mhc_layer_norm_backward_workspace_bytes(T: int, d: int) -> int:
@@ -512,20 +533,14 @@ def mhc_layer_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, works
     import torch
     where = "mhc_layer_norm_backward"
     T, d = _rows(where, "x", x)
-    for name, t, shape in (("weight", weight, (d,)), ("mean", mean, (T,)), ("rstd", rstd, (T,)), ("dy", dy, (T, d)),
-                           ("dx", dx, (T, d)), ("dweight", dweight, (d,)), ("dbias", dbias, (d,))):
-        _shape(where, name, t, shape)
-    dev, f32 = x.device, torch.float32
-    dt = _dt(x)
-    p = [_ptr(t, name, x.dtype, dev) for name, t in (("x", x), ("dy", dy), ("dx", dx))]
-    q = [_ptr(t, name, f32, dev) for name, t in (("weight", weight), ("mean", mean), ("rstd", rstd),
-                                                 ("dweight", dweight), ("dbias", dbias))]
+    dt, xt, f32, dev = _dt(x), x.dtype, torch.float32, x.device
+    px, pw, pm, pr, pg, pdx, pdw, pdb = _pointers(where, dev, (
+        ("x", x, x.shape, xt), ("weight", weight, (d,), f32), ("mean", mean, (T,), f32), ("rstd", rstd, (T,), f32),
+        ("dy", dy, x.shape, xt), ("dx", dx, x.shape, xt), ("dweight", dweight, (d,), f32),
+        ("dbias", dbias, (d,), f32)))
     ws, nbytes = _workspace(workspace, dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.mhc_layer_norm_backward(p[0], q[0], q[1], q[2], T, d, dt, p[1], p[2], q[3], q[4], ws, nbytes,
-                                         _stream(stream, dev))
-    _check(st, where)
+    _call(where, load_library().mhc_layer_norm_backward, dev, stream,
+          (px, pw, pm, pr, T, d, dt, pg, pdx, pdw, pdb, ws, nbytes))
 
 
 def _dt_of(dtype) -> int:
@@ -556,19 +571,13 @@ def mhc_linear(x, W, bias, y, act: int = ACT_NONE, residual=None, z=None, worksp
     where = "mhc_linear"
     T, K = _rows(where, "x", x)
     N = _rows(where, "W", W)[0]
-    for name, t, shape in (("W", W, (N, K)), ("bias", bias, (N,)), ("y", y, (T, N)), ("residual", residual, (T, N)),
-                           ("z", z, (T, N))):
-        _shape(where, name, t, shape)
-    dev = x.device
-    dt = _dt(x)
-    p = [_ptr(t, name, x.dtype, dev) for name, t in (("x", x), ("W", W), ("residual", residual), ("y", y), ("z", z))]
-    pb = _ptr(bias, "bias", torch.float32, dev)
+    dt, xt, dev, out = _dt(x), x.dtype, x.device, (T, N)
+    px, pw, pb, pr, py, pz = _pointers(where, dev, (
+        ("x", x, x.shape, xt), ("W", W, (N, K), xt), ("bias", bias, (N,), torch.float32),
+        ("residual", residual, out, xt), ("y", y, out, xt), ("z", z, out, xt)))
     ws, nbytes = _workspace(workspace, dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.mhc_linear(p[0], p[1], pb, p[2], T, K, N, int(act), dt, p[3], p[4], ws, nbytes,
-                            _stream(stream, dev))
-    _check(st, where)
+    _call(where, load_library().mhc_linear, dev, stream,
+          (px, pw, pb, pr, T, K, N, int(act), dt, py, pz, ws, nbytes))
 
 
 def mhc_linear_backward_workspace_bytes(T: int, K: int, N: int, dtype) -> int:
@@ -586,19 +595,13 @@ def mhc_linear_backward(x, W, z, dy, dx, dW, dbias, workspace, act: int = ACT_NO
     where = "mhc_linear_backward"
     T, K = _rows(where, "x", x)
     N = _rows(where, "W", W)[0]
-    for name, t, shape in (("W", W, (N, K)), ("z", z, (T, N)), ("dy", dy, (T, N)), ("dx", dx, (T, K)),
-                           ("dW", dW, (N, K)), ("dbias", dbias, (N,))):
-        _shape(where, name, t, shape)
-    dev = x.device
-    dt = _dt(x)
-    p = [_ptr(t, name, x.dtype, dev) for name, t in (("x", x), ("W", W), ("z", z), ("dy", dy), ("dx", dx), ("dW", dW))]
-    pb = _ptr(dbias, "dbias", torch.float32, dev)
+    dt, xt, dev, out = _dt(x), x.dtype, x.device, (T, N)
+    px, pw, pz, pg, pdx, pdw, pdb = _pointers(where, dev, (
+        ("x", x, x.shape, xt), ("W", W, (N, K), xt), ("z", z, out, xt), ("dy", dy, out, xt), ("dx", dx, x.shape, xt),
+        ("dW", dW, (N, K), xt), ("dbias", dbias, (N,), torch.float32)))
     ws, nbytes = _workspace(workspace, dev)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.mhc_linear_backward(p[0], p[1], p[2], T, K, N, int(act), dt, p[3], p[4], p[5], pb, ws, nbytes,
-                                     _stream(stream, dev))
-    _check(st, where)
+    _call(where, load_library().mhc_linear_backward, dev, stream,
+          (px, pw, pz, T, K, N, int(act), dt, pg, pdx, pdw, pdb, ws, nbytes))
 
 
 def mhc_amax_gain(H_layers, gain, stream=None):

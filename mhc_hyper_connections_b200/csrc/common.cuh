@@ -34,6 +34,44 @@ __device__ __forceinline__ void st_v4(void* p, uint4 v) {
                  :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// Eight 16-bit elements from element `at` of an array of `total`, wherever it lies: the two 16-byte
+// words around them, shifted together.  Elements past the array's end read as zero, and no word is
+// read that is not wholly inside it.
+__device__ __forceinline__ uint4 ld_shifted_v4(const __nv_bfloat16* p, int64_t at, int64_t total) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p + at), end = reinterpret_cast<uintptr_t>(p + total);
+    const uint32_t m = (uint32_t)(a & 15);
+    const uintptr_t lo = a - m, hi = lo + (m ? 32 : 16);
+    uint32_t w[8] = {};
+    if (lo >= reinterpret_cast<uintptr_t>(p) && hi <= end) {
+        const uint4 v = ld_stream_v4(reinterpret_cast<const void*>(lo));
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        if (m) {
+            const uint4 u = ld_stream_v4(reinterpret_cast<const void*>(lo + 16));
+            w[4] = u.x; w[5] = u.y; w[6] = u.z; w[7] = u.w;
+        }
+    } else {
+        // at either end of the array: the elements one by one, in place already
+        const unsigned short* e = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (at + j < total) w[j >> 1] |= (uint32_t)__ldg(e + at + j) << (16 * (j & 1));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (m & 8) {
+#pragma unroll
+        for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+    }
+    if (m & 4) {
+#pragma unroll
+        for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+    }
+    if (m & 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A bf16 pair packed in a 32-bit word as an fp32 pair (element 0 first).
 __device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));

@@ -29,9 +29,21 @@ int64_t dz_runs(int64_t T, int N) {
     return std::min(want, (T + DZ_ROWS - 1) / DZ_ROWS);
 }
 
+// Loads of VEC columns at (t, c): 16-byte rows, or bf16 rows wherever they lie (SHIFT)
+template <typename T, int VEC, bool SHIFT>
+__device__ __forceinline__ void dz_load(const T* __restrict__ p, int64_t t, int64_t c, int64_t Tn, int N, float* f) {
+    if constexpr (SHIFT) {
+        Vec16<T>::unpack(ld_shifted_v4(p, t * N + c, Tn * N), f);
+    } else if constexpr (VEC > 1) {
+        Vec16<T>::unpack(ld_stream_v4(p + t * N + c), f);
+    } else {
+        f[0] = to_f32(__ldg(p + t * N + c));
+    }
+}
+
 // A thread takes VEC columns and four tokens at a time (their loads are in flight together).  dz
 // null: column sums only; part null: no sums.
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool SHIFT>
 __global__ void __launch_bounds__(DZ_COLS* DZ_ROWS)
 dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, int64_t run, T* __restrict__ dz,
           int64_t ld, float* __restrict__ part) {
@@ -44,32 +56,12 @@ dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, 
     if (c < N) {
         for (int64_t t = t0 + ty; t < t1; t += DZ_ROWS * U) {
             float g[U][VEC], zf[U][VEC];
-            if constexpr (VEC > 1) {
-                uint4 rg[U], rz[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int64_t tu = t + u * DZ_ROWS;
-                    rg[u] = rz[u] = make_uint4(0, 0, 0, 0);
-                    if (tu < t1) {
-                        rg[u] = ld_stream_v4(dy + tu * N + c);
-                        if constexpr (ACT != ACT_NONE) rz[u] = ld_stream_v4(z + tu * N + c);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    Vec16<T>::unpack(rg[u], g[u]);
-                    Vec16<T>::unpack(rz[u], zf[u]);
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int64_t tu = t + u * DZ_ROWS;
-                    g[u][0] = zf[u][0] = 0.f;
-                    if (tu < t1) {
-                        g[u][0] = to_f32(__ldg(dy + tu * N + c));
-                        if constexpr (ACT != ACT_NONE) zf[u][0] = to_f32(__ldg(z + tu * N + c));
-                    }
-                }
+            for (int u = 0; u < U; ++u) {
+                const int64_t tu = t + u * DZ_ROWS;
+                if (tu >= t1) break;
+                dz_load<T, VEC, SHIFT>(dy, tu, c, Tn, N, g[u]);
+                if constexpr (ACT != ACT_NONE) dz_load<T, VEC, SHIFT>(z, tu, c, Tn, N, zf[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -84,7 +76,7 @@ dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, 
                 }
                 if (dz) {
                     if constexpr (VEC > 1) {
-                        st_v4(dz + tu * ld + c, Vec16<T>::pack(g[u]));
+                        st_v4(dz + tu * ld + c, Vec16<T>::pack(g[u]));      // may fill up the row's padding
                     } else {
                         store_elem(dz + tu * ld + c, g[u][0]);
                     }
@@ -125,7 +117,7 @@ sum_rows_kernel(const float* __restrict__ part, int64_t P, int N, float* __restr
     }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool SHIFT>
 void start_dz(const LinearArgs& a, void* dz, int64_t ld, int64_t run, int64_t rows, float* sums) {
     const int cols = DZ_COLS * VEC;
     const dim3 grid((unsigned)((a.N + (int64_t)cols - 1) / cols), (unsigned)rows);
@@ -134,11 +126,11 @@ void start_dz(const LinearArgs& a, void* dz, int64_t ld, int64_t run, int64_t ro
                                                        a.N, run, static_cast<T*>(dz), ld, sums);
     };
     switch (a.act) {
-        case ACT_RELU: go(dz_kernel<T, VEC, ACT_RELU>); break;
-        case ACT_GELU: go(dz_kernel<T, VEC, ACT_GELU>); break;
-        case ACT_GELU_TANH: go(dz_kernel<T, VEC, ACT_GELU_TANH>); break;
-        case ACT_SILU: go(dz_kernel<T, VEC, ACT_SILU>); break;
-        default: go(dz_kernel<T, VEC, ACT_NONE>); break;
+        case ACT_RELU: go(dz_kernel<T, VEC, ACT_RELU, SHIFT>); break;
+        case ACT_GELU: go(dz_kernel<T, VEC, ACT_GELU, SHIFT>); break;
+        case ACT_GELU_TANH: go(dz_kernel<T, VEC, ACT_GELU_TANH, SHIFT>); break;
+        case ACT_SILU: go(dz_kernel<T, VEC, ACT_SILU, SHIFT>); break;
+        default: go(dz_kernel<T, VEC, ACT_NONE, SHIFT>); break;
     }
 }
 
@@ -149,10 +141,12 @@ cudaError_t launch_dz(const LinearArgs& a, void* dz, int64_t ld, float* part) {
     const int64_t run = ((a.T + runs - 1) / runs + DZ_ROWS - 1) / DZ_ROWS * DZ_ROWS;
     const int64_t rows = (a.T + run - 1) / run;      // runs that hold tokens
     float* sums = a.dbias ? (rows == 1 ? a.dbias : part) : nullptr;
-    if (a.N % V == 0 && ld % V == 0 && (uintptr_t)a.dy % 16 == 0 && (uintptr_t)a.z % 16 == 0)
-        start_dz<T, V>(a, dz, ld, run, rows, sums);
+    if (a.N % V == 0 && (uintptr_t)a.dy % 16 == 0 && (uintptr_t)a.z % 16 == 0)
+        start_dz<T, V, false>(a, dz, ld, run, rows, sums);
+    else if constexpr (sizeof(T) == 2)
+        start_dz<T, V, true>(a, dz, ld, run, rows, sums);
     else
-        start_dz<T, 1>(a, dz, ld, run, rows, sums);
+        start_dz<T, 1, false>(a, dz, ld, run, rows, sums);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.dbias && rows > 1)
         e = launch_pdl(sum_rows_kernel, dim3((unsigned)((a.N + (int64_t)31) / 32)), dim3(256), 0, a.stream, part,
@@ -160,38 +154,82 @@ cudaError_t launch_dz(const LinearArgs& a, void* dz, int64_t ld, float* part) {
     return e;
 }
 
-cudaError_t product(const GemmArgs& g) { return gemm_tc_ok(g) ? launch_gemm_tc(g) : launch_gemm_generic(g); }
-
-// regions of the backward's workspace, in bytes
-struct BackwardLayout {
-    size_t dz, part, total;
-    int64_t ld;                        // elements per row of dz: 16-byte rows
+// A copy of bf16 rows with each row on a 16-byte boundary, for the tensor-core products of operands
+// whose row length or address is not a multiple of 16 bytes.
+struct PadJob {
+    const __nv_bfloat16* src;
+    __nv_bfloat16* dst;
+    int64_t rows, ld;                  // ld: elements per row of dst, the row length rounded up to 8
+    int cols;
 };
 
-BackwardLayout backward_regions(int64_t T, int K, int N, DType dt) {
-    BackwardLayout L{};
+__global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ PadJob a, const __grid_constant__ PadJob b) {
+    const PadJob& j = blockIdx.y ? b : a;
+    const int64_t per = j.ld / 8, total = j.rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per, c = (i - row * per) * 8;
+        st_v4(j.dst + row * j.ld + c, ld_shifted_v4(j.src, row * j.cols + c, j.rows * j.cols));
+    }
+}
+
+cudaError_t pad_rows(const PadJob& a, const PadJob& b, cudaStream_t s) {
+    const int64_t n = std::max(a.rows * a.ld, b.rows * b.ld) / 8;
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 8 * 148);
+    pad_rows_kernel<<<dim3(blocks, b.rows ? 2 : 1), 256, 0, s>>>(a, b);
+    return cudaGetLastError();
+}
+
+int64_t padded(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+cudaError_t product(const GemmArgs& g) { return gemm_tc_ok(g) ? launch_gemm_tc(g) : launch_gemm_generic(g); }
+
+// Regions of the workspaces, in bytes.  bf16 rows of K elements that are not a multiple of 16 bytes
+// are copied to padded ones (x and W).
+struct Regions {
+    size_t x, W, dz, part, total;
+    int64_t ldk, ldn;                  // elements per row of the padded x and W, and of dz
+    bool pad;
+};
+
+Regions regions(int64_t T, int K, int N, DType dt, bool backward) {
+    Regions L{};
     const size_t es = dt == BF16 ? 2 : 4;
-    const int64_t v = 16 / es;
-    (void)K;
-    L.ld = ((int64_t)N + v - 1) / v * v;
-    L.dz = 0;
-    L.part = round256((size_t)T * L.ld * es);
-    L.total = L.part + round256((size_t)dz_runs(T, N) * N * 4);
+    L.pad = dt == BF16 && K % 8 != 0;
+    L.ldk = L.pad ? padded(K) : K;
+    L.ldn = dt == BF16 ? padded(N) : N;
+    size_t off = 0;
+    auto take = [&](size_t bytes) { const size_t at = off; off += round256(bytes); return at; };
+    if (L.pad) {
+        L.x = take((size_t)T * L.ldk * es);
+        L.W = take((size_t)N * L.ldk * es);
+    }
+    if (backward) {
+        L.dz = take((size_t)T * L.ldn * es);
+        L.part = take((size_t)dz_runs(T, N) * N * 4);
+    }
+    L.total = off;
     return L;
 }
 
 }  // namespace
 
-size_t linear_workspace(int64_t T, int K, int N, DType dt) {
-    (void)T; (void)K; (void)N; (void)dt;
-    return 0;
-}
+size_t linear_workspace(int64_t T, int K, int N, DType dt) { return regions(T, K, N, dt, false).total; }
 
-size_t linear_backward_workspace(int64_t T, int K, int N, DType dt) { return backward_regions(T, K, N, dt).total; }
+size_t linear_backward_workspace(int64_t T, int K, int N, DType dt) { return regions(T, K, N, dt, true).total; }
 
 cudaError_t launch_linear(const LinearArgs& a) {
+    const Regions L = regions(a.T, a.K, a.N, a.dt, false);
+    unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     GemmArgs g{};
-    g.A = a.x; g.lda = a.K; g.B = a.W; g.ldb = a.K;
+    g.A = a.x; g.B = a.W;
+    g.lda = g.ldb = L.ldk;
+    if (L.pad) {
+        const PadJob x{static_cast<const __nv_bfloat16*>(a.x), reinterpret_cast<__nv_bfloat16*>(ws + L.x), a.T, L.ldk, a.K};
+        const PadJob w{static_cast<const __nv_bfloat16*>(a.W), reinterpret_cast<__nv_bfloat16*>(ws + L.W), a.N, L.ldk, a.K};
+        const cudaError_t e = pad_rows(x, w, a.stream);
+        if (e != cudaSuccess) return e;
+        g.A = x.dst; g.B = w.dst;
+    }
     g.M = a.T; g.N = a.N; g.K = a.K;
     g.bias = a.bias; g.residual = a.residual; g.act = a.act; g.D = a.y; g.z = a.z;
     g.dt = a.dt; g.stream = a.stream;
@@ -199,30 +237,42 @@ cudaError_t launch_linear(const LinearArgs& a) {
 }
 
 cudaError_t launch_linear_backward(const LinearArgs& a) {
-    const BackwardLayout L = backward_regions(a.T, a.K, a.N, a.dt);
+    const Regions L = regions(a.T, a.K, a.N, a.dt, true);
     unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     const bool products = a.dx || a.dW;
-    // dz is dy itself without an activation
-    void* dz = a.act != ACT_NONE && products ? ws + L.dz : nullptr;
+    // dz is dy itself without an activation, unless the tensor cores need its rows on 16-byte boundaries
+    const bool copy = a.act != ACT_NONE || (a.dt == BF16 && (a.N % 8 != 0 || (uintptr_t)a.dy % 16 != 0));
+    void* dz = copy && products ? ws + L.dz : nullptr;
     cudaError_t e = cudaSuccess;
     if (dz || a.dbias) {
         float* part = reinterpret_cast<float*>(ws + L.part);
-        e = a.dt == BF16 ? launch_dz<__nv_bfloat16>(a, dz, L.ld, part) : launch_dz<float>(a, dz, L.ld, part);
+        e = a.dt == BF16 ? launch_dz<__nv_bfloat16>(a, dz, L.ldn, part) : launch_dz<float>(a, dz, L.ldn, part);
+    }
+    const void* x = a.x;
+    const void* W = a.W;
+    if (e == cudaSuccess && L.pad && products) {
+        const PadJob none{};
+        const PadJob jx{static_cast<const __nv_bfloat16*>(a.x), reinterpret_cast<__nv_bfloat16*>(ws + L.x), a.T, L.ldk, a.K};
+        const PadJob jw{static_cast<const __nv_bfloat16*>(a.W), reinterpret_cast<__nv_bfloat16*>(ws + L.W), a.N, L.ldk, a.K};
+        e = pad_rows(a.dx ? jw : jx, a.dx && a.dW ? jx : none, a.stream);
+        x = jx.dst;
+        W = jw.dst;
     }
     GemmArgs g{};
     g.A = dz ? dz : a.dy;
-    g.lda = dz ? L.ld : a.N;
+    g.lda = dz ? L.ldn : a.N;
     g.dt = a.dt; g.stream = a.stream; g.act = ACT_NONE;
     g.b_mn = true;
+    g.ldb = L.ldk;
     if (e == cudaSuccess && a.dx) {          // dx[t][k] = sum_n dz[t][n] W[n][k]
-        g.B = a.W; g.ldb = a.K;
+        g.B = W;
         g.M = a.T; g.N = a.K; g.K = a.N;
         g.D = a.dx;
         e = product(g);
     }
     if (e == cudaSuccess && a.dW) {          // dW[n][k] = sum_t dz[t][n] x[t][k]
         g.a_mn = true;
-        g.B = a.x; g.ldb = a.K;
+        g.B = x;
         g.M = a.N; g.N = a.K; g.K = a.T;
         g.D = a.dW;
         e = product(g);

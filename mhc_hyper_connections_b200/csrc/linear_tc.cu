@@ -23,6 +23,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -41,7 +42,7 @@ namespace lintc {
 using namespace ptx;
 using bf16 = __nv_bfloat16;
 
-constexpr int BK = 64;                  // K per stage: one 128-byte row
+constexpr int BK = 64;                  // K of a block: one 128-byte row
 constexpr int ROW = 128;                // bytes
 constexpr int BLK = 64 * ROW;           // a 64 x 64 box of an operand whose M / N index is contiguous
 constexpr int THREADS = 320;
@@ -49,7 +50,6 @@ constexpr int EPI = 8;                  // epilogue warps: two per TMEM lane qua
 constexpr unsigned long long kWaitNs = 1000000000ull;    // 1 s per wait
 constexpr unsigned long long kDrainNs = 2000000000ull;   // 2 s for the drains at exit
 constexpr unsigned long long kLandNs = 2000000ull;       // after a failed wait: loads in flight land
-constexpr uint32_t kSuspendNs = 20000;
 
 enum : unsigned { E_STAGE = 1u, E_ACC = 2u, E_DRAIN = 4u };
 
@@ -59,25 +59,21 @@ __host__ __device__ constexpr uint32_t idesc(int mm, int nn, bool a_mn, bool b_m
            ((uint32_t)(nn >> 3) << 17) | ((uint32_t)(mm >> 4) << 24);
 }
 
-__device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(kSuspendNs) : "memory");
-    return ok != 0;
-}
-
 struct Waiter {
     volatile int* abort_flag;
     unsigned long long limit_ns;
     // true when the phase completed; false when the CTA is aborting or the wait expired
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, unsigned code,
                                                bool honour_abort = true) const {
-        if (mbar_try_cluster(bar, parity)) return true;
+        // the timer is read only after tries that no healthy wait needs: reading it costs more than
+        // a pipeline step
+        for (int i = 0; i < 256; ++i) {
+            if (mbar_try(bar, parity)) return true;
+            if (honour_abort && *abort_flag) return false;
+        }
         const uint64_t t0 = gtimer();
         while (true) {
-            if (mbar_try_sleep(bar, parity)) return true;
+            if (mbar_try(bar, parity)) return true;
             if (honour_abort && *abort_flag) return false;
             if (gtimer() - t0 > limit_ns) {
                 atomicOr(&g_linear_status, code);
@@ -86,7 +82,35 @@ struct Waiter {
             }
         }
     }
+    // the whole warp's answer, with every lane past the wait
+    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity, unsigned code, bool honour_abort = true) const {
+        return __all_sync(0xffffffffu, (*this)(bar, parity, code, honour_abort));
+    }
 };
+
+// Position in a ring of NS stages: the slot, and the parity of the slot's current round.  Waiting
+// for the opposite parity is waiting for the previous round, which before the first one is over.
+template <int NS>
+struct Ring {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == NS) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// One lane of a converged warp.  The issue loops below are walked by whole warps and only the
+// instructions that start asynchronous work sit under this predicate: the compiler then keeps
+// descriptors and addresses in uniform registers.  Walked by one lane alone, a K step of the MMA
+// loop took 620 cycles to issue, more than its MMAs take to run.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 
 __device__ __forceinline__ void pause_ns(unsigned long long ns) {
     const uint64_t t0 = gtimer();
@@ -123,16 +147,30 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
-// the descriptor of K16 step k of an operand's rows
+// The descriptor of an operand's rows in stage 0, and the descriptor units (16 bytes) from one K16
+// step to the next: 32 bytes along a row, or 16 rows of a box whose rows run along M / N.
 template <bool MN>
-__device__ __forceinline__ uint64_t step_desc(uint32_t base, int k) {
-    return MN ? sw128_desc_mn(base + k * 2048, BLK, 1024) : sw128_desc(base + k * 32);
+__device__ __forceinline__ uint64_t base_desc(uint32_t base) {
+    return MN ? sw128_desc_mn(base, BLK, 1024) : sw128_desc(base);
+}
+template <bool MN> constexpr uint32_t K16 = MN ? 2048 / 16 : 32 / 16;
+
+// 32 lanes x 8 consecutive 32-bit columns, waiting for the load
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&f)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[i]);
 }
 
 struct Maps {
@@ -152,8 +190,13 @@ struct Epilogue {
 
 template <int BN>
 struct PairCfg {
-    static constexpr int A_BYTES = 128 * ROW, B_BYTES = BN / 2 * ROW, STAGE = A_BYTES + B_BYTES;
-    static constexpr int NS = 196608 / STAGE;                  // 6 stages at BN = 256, 8 at BN = 128
+    static constexpr int A_BYTES = 128 * ROW, B_BYTES = BN / 2 * ROW, BLOCK = A_BYTES + B_BYTES;
+    // Blocks per stage: a stage's waits and commits take about as long to issue as 8 MMAs of N = 128
+    // (T = 256, 16384 -> 4096 at BN = 128: 67 us with one block per stage, 54 with two); at N = 256 the
+    // MMAs of one block cover them, and finer stages are refilled sooner (79 us with one, 83 with two)
+    static constexpr int KS = BN == 256 ? 1 : 2;
+    static constexpr int STAGE = KS * BLOCK;
+    static constexpr int NS = 196608 / STAGE;                  // 6 stages at BN = 256, 4 at BN = 128
     static constexpr int OUT = EPI * 32 * ROW;                 // a 32 x 64 bf16 block per epilogue warp
     static constexpr int SMEM = NS * STAGE + OUT + 1024;       // + alignment slack
     static constexpr int TMEM_COLS = 512;                      // all of it, so both CTAs hold column 0
@@ -175,10 +218,10 @@ __device__ __forceinline__ void tile_at(int64_t i, int mt, int nt, int& m, int& 
 
 template <int BN, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue ep, int64_t M, int64_t N, int ksteps, int mt,
+gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue ep, int64_t M, int64_t N, int kblocks, int mt,
                  int nt, unsigned long long wait_ns) {
     using C = PairCfg<BN>;
-    constexpr int NS = C::NS;
+    constexpr int NS = C::NS, KS = C::KS;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) uint64_t bars[2 * NS + 5];
@@ -192,7 +235,7 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
     const Waiter wait{&abort_flag, wait_ns};
     const Waiter drain{&abort_flag, wait_ns > kDrainNs ? wait_ns : kDrainNs};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = cluster_ctarank(), base = smem_u32(sm);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -217,67 +260,83 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
     const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int64_t i = first; ok && i < tiles; i += stride) {
-                int m, n;
-                tile_at(i, mt, nt, m, n);
-                const int m0 = m * 256 + (int)rank * 128, n0 = n * BN + (int)rank * (BN / 2);
-                for (int ks = 0; ks < ksteps; ++ks, ++it) {
-                    const int s = it % NS;
-                    if (it >= NS && !(ok = wait(empty(s), (uint32_t)(it / NS - 1) & 1u, E_STAGE))) break;
-                    if (rank == 0) mbar_arrive_tx(full(s), 2 * C::STAGE);
+        Ring<NS> ring;
+        bool ok = true;
+        for (int64_t i = first; ok && i < tiles; i += stride) {
+            int m, n;
+            tile_at(i, mt, nt, m, n);
+            const int m0 = m * 256 + (int)rank * 128, n0 = n * BN + (int)rank * (BN / 2);
+            for (int kb = 0; kb < kblocks; kb += KS, ring.next()) {
+                const int s = ring.s;
+                if (!(ok = wait.warp(empty(s), ring.parity ^ 1u, E_STAGE))) break;
+                if (elect_one()) {
+                    const int nb = kblocks - kb < KS ? kblocks - kb : KS;
+                    if (rank == 0) mbar_arrive_tx(full(s), 2 * C::BLOCK * nb);
                     const uint32_t bar = mapa(full(s), 0);
-                    const uint32_t a = smem_u32(sm + s * C::STAGE), b = a + C::A_BYTES;
-                    if constexpr (A_MN) {
-                        tma_load_pair(a, &maps.a, bar, m0, ks * BK);
-                        tma_load_pair(a + BLK, &maps.a, bar, m0 + 64, ks * BK);
-                    } else {
-                        tma_load_pair(a, &maps.a, bar, ks * BK, m0);
-                    }
-                    if constexpr (B_MN) {
 #pragma unroll
-                        for (int j = 0; j < BN / 128; ++j)
-                            tma_load_pair(b + j * BLK, &maps.b, bar, n0 + 64 * j, ks * BK);
-                    } else {
-                        tma_load_pair(b, &maps.b, bar, ks * BK, n0);
+                    for (int u = 0; u < KS; ++u) {
+                        if (u >= nb) break;
+                        const uint32_t a = base + s * C::STAGE + u * C::BLOCK, b = a + C::A_BYTES;
+                        const int k = (kb + u) * BK;
+                        if constexpr (A_MN) {
+                            tma_load_pair(a, &maps.a, bar, m0, k);
+                            tma_load_pair(a + BLK, &maps.a, bar, m0 + 64, k);
+                        } else {
+                            tma_load_pair(a, &maps.a, bar, k, m0);
+                        }
+                        if constexpr (B_MN) {
+#pragma unroll
+                            for (int j = 0; j < BN / 128; ++j) tma_load_pair(b + j * BLK, &maps.b, bar, n0 + 64 * j, k);
+                        } else {
+                            tma_load_pair(b, &maps.b, bar, k, n0);
+                        }
                     }
                 }
+                __syncwarp();
             }
-            // the last stages' MMAs have signalled this CTA too before it may exit
-            for (int j = it < NS ? 0 : it - NS; ok && j < it; ++j)
-                ok = wait(empty(j % NS), (uint32_t)(j / NS) & 1u, E_STAGE);
-            if (!ok) pause_ns(kLandNs);
         }
+        // the last stages' MMAs have signalled this CTA too before it may exit (a stage never used
+        // counts as free)
+        for (int j = 0; ok && j < NS; ++j, ring.next()) ok = wait.warp(empty(ring.s), ring.parity ^ 1u, E_STAGE);
+        if (!ok) pause_ns(kLandNs);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t ID = idesc(256, BN, A_MN, B_MN);
-            int it = 0, tc = 0;
+            const uint64_t da0 = base_desc<A_MN>(base), db0 = base_desc<B_MN>(base + C::A_BYTES);
+            Ring<NS> ring;
+            int tc = 0;
             bool ok = true;
             for (int64_t i = first; ok && i < tiles; i += stride, ++tc) {
                 const int buf = tc & 1;
-                if (tc >= 2 && !(ok = wait(acce(buf), (uint32_t)((tc >> 1) - 1) & 1u, E_ACC))) break;
+                if (!(ok = wait.warp(acce(buf), ((uint32_t)(tc >> 1) & 1u) ^ 1u, E_ACC))) break;
                 tc_fence_after();
-                for (int ks = 0; ks < ksteps; ++ks, ++it) {
-                    const int s = it % NS;
-                    if (!(ok = wait(full(s), (uint32_t)(it / NS) & 1u, E_STAGE))) break;
+                for (int kb = 0; kb < kblocks; kb += KS, ring.next()) {
+                    const int s = ring.s;
+                    if (!(ok = wait.warp(full(s), ring.parity, E_STAGE))) break;
                     tc_fence_after();
-                    const uint32_t a = smem_u32(sm + s * C::STAGE), b = a + C::A_BYTES;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        mma_pair(tm + buf * BN, step_desc<A_MN>(a, k), step_desc<B_MN>(b, k), ID,
-                                 (ks > 0 || k > 0) ? 1u : 0u);
-                    mma_commit_pair(empty(s));
+                        for (int u = 0; u < KS; ++u) {
+                            if (kb + u >= kblocks) break;
+                            const uint32_t off = (uint32_t)(s * (C::STAGE >> 4) + u * (C::BLOCK >> 4));
+#pragma unroll
+                            for (int k = 0; k < BK / 16; ++k)
+                                mma_pair(tm + buf * BN, da0 + off + k * K16<A_MN>, db0 + off + k * K16<B_MN>, ID,
+                                         (kb > 0 || u > 0 || k > 0) ? 1u : 0u);
+                        }
+                        mma_commit_pair(empty(s));
+                        if (kb + KS >= kblocks) mma_commit_pair(accf(buf));
+                    }
+                    __syncwarp();
                 }
-                if (ok) mma_commit_pair(accf(buf));
             }
             if (!ok) {
                 // every MMA issued so far: TMEM must be idle before it is freed
-                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                             :: "r"(drained) : "memory");
-                drain(drained, 0u, E_DRAIN, false);
+                if (elect_one())
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                                 :: "r"(drained) : "memory");
+                drain.warp(drained, 0u, E_DRAIN, false);
             }
         }
         __syncwarp();
@@ -292,39 +351,37 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
             int m, n;
             tile_at(i, mt, nt, m, n);
             const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q;
-            if (!__all_sync(0xffffffffu, wait(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC))) break;
+            if (!wait.warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC)) break;
             tc_fence_after();
+#pragma unroll 1
             for (int cc = 0; cc < BN / 2; cc += 64) {
                 const int64_t c0 = (int64_t)n * BN + h * (BN / 2) + cc;
+                if (c0 >= N || r0 >= M) continue;
                 float v[64];
                 tmem_ld32(tq + buf * BN + h * (BN / 2) + cc, reinterpret_cast<float(&)[32]>(v[0]));
                 tmem_ld32(tq + buf * BN + h * (BN / 2) + cc + 32, reinterpret_cast<float(&)[32]>(v[32]));
-                if (c0 >= N || r0 >= M) continue;
                 // this warp's 32 x 64 block between registers (a row per lane) and memory (128 bytes
                 // of a row per eight lanes), through shared memory swizzled by 16-byte chunks
-                auto lane_chunk = [&](int j) {
-                    return reinterpret_cast<uint4*>(out + lane * ROW + ((j ^ (lane & 7)) << 4));
-                };
+                auto at = [&](int r, int j) { return out + r * ROW + ((j ^ (r & 7)) << 4); };
                 auto put = [&](bf16* dst) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) *lane_chunk(j) = Vec16<bf16>::pack(v + 8 * j);
+                    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at(lane, j)) = Vec16<bf16>::pack(v + 8 * j);
                     __syncwarp();
                     if (ep.vec) {
 #pragma unroll
                         for (int p = 0; p < 8; ++p) {
                             const int r = 4 * p + (lane >> 3), j = lane & 7;
                             if (r0 + r < M && c0 + 8 * j < N)
-                                st_v4(dst + (r0 + r) * N + c0 + 8 * j,
-                                      *reinterpret_cast<const uint4*>(out + r * ROW + ((j ^ (r & 7)) << 4)));
+                                st_v4(dst + (r0 + r) * N + c0 + 8 * j, *reinterpret_cast<const uint4*>(at(r, j)));
                         }
                     } else {
+#pragma unroll 2
                         for (int r = 0; r < 32 && r0 + r < M; ++r)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 const int c = lane + 32 * u;
                                 if (c0 + c < N)
-                                    dst[(r0 + r) * N + c0 + c] = *reinterpret_cast<const bf16*>(
-                                        out + r * ROW + (((c >> 3) ^ (r & 7)) << 4) + 2 * (c & 7));
+                                    dst[(r0 + r) * N + c0 + c] = reinterpret_cast<const bf16*>(at(r, c >> 3))[c & 7];
                             }
                     }
                     __syncwarp();
@@ -334,40 +391,41 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
                     for (int j = 0; j < 64; ++j) v[j] += c0 + j < N ? __ldg(ep.bias + c0 + j) : 0.f;
                 }
                 if (ep.z) put(ep.z);
-                with_act(ep.act, [&](auto kind) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = act_value<kind(), true>(v[j]);
-                });
                 if (ep.residual) {
                     if (ep.vec) {
 #pragma unroll
                         for (int p = 0; p < 8; ++p) {
                             const int r = 4 * p + (lane >> 3), j = lane & 7;
                             if (r0 + r < M && c0 + 8 * j < N)
-                                *reinterpret_cast<uint4*>(out + r * ROW + ((j ^ (r & 7)) << 4)) =
+                                *reinterpret_cast<uint4*>(at(r, j)) =
                                     ld_stream_v4(ep.residual + (r0 + r) * N + c0 + 8 * j);
                         }
                     } else {
+#pragma unroll 2
                         for (int r = 0; r < 32 && r0 + r < M; ++r)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 const int c = lane + 32 * u;
                                 if (c0 + c < N)
-                                    *reinterpret_cast<bf16*>(out + r * ROW + (((c >> 3) ^ (r & 7)) << 4) +
-                                                             2 * (c & 7)) = ep.residual[(r0 + r) * N + c0 + c];
+                                    reinterpret_cast<bf16*>(at(r, c >> 3))[c & 7] = ep.residual[(r0 + r) * N + c0 + c];
                             }
                     }
                     __syncwarp();
+                }
+                with_act(ep.act, [&](auto kind) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j] = act_value<kind(), true>(v[j]);
+                });
+                if (ep.residual) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         float f[8];
-                        Vec16<bf16>::unpack(*lane_chunk(j), f);
+                        Vec16<bf16>::unpack(*reinterpret_cast<uint4*>(at(lane, j)), f);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) v[8 * j + e] += f[e];
                     }
-                    __syncwarp();
                 }
-                put(ep.D);
+                put(ep.D);               // a lane overwrites its own row of the residual
             }
             tc_fence_before();
             __syncwarp();
@@ -387,8 +445,13 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
 
 template <int BN>
 struct SplitCfg {
-    static constexpr int A_BYTES = 128 * ROW, B_BYTES = BN * ROW, STAGE = A_BYTES + B_BYTES;
-    static constexpr int NS = 110592 / STAGE;                  // two CTAs per SM
+    static constexpr int A_BYTES = 128 * ROW, B_BYTES = BN * ROW, BLOCK = A_BYTES + B_BYTES;
+    // two CTAs per SM up to BN = 64, one above; two blocks per stage where three such stages fit
+    static constexpr int PER_SM = BN > 64 ? 1 : 2;
+    static constexpr int ROOM = 221184 / PER_SM;
+    static constexpr int KS = 6 * BLOCK <= ROOM ? 2 : 1;
+    static constexpr int STAGE = KS * BLOCK;
+    static constexpr int NS = ROOM / STAGE;
     static constexpr int SMEM = NS * STAGE + 1024;
     static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
     static_assert(NS * STAGE >= BN * 128 * 4, "the partial tile fits the stages");
@@ -397,11 +460,11 @@ struct SplitCfg {
 // D[c][r] = sum_k A(r, k) B(c, k), c < Nc, r < Mr, rows of Mr elements: A's side is the contiguous
 // one.  bias belongs to r.
 template <int BN, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(THREADS, 2)
-gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue ep, int64_t Mr, int64_t Nc, int ksteps, int mt,
+__global__ void __launch_bounds__(THREADS, SplitCfg<BN>::PER_SM)
+gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue ep, int64_t Mr, int64_t Nc, int kblocks, int mt,
                   int S, unsigned long long wait_ns) {
     using C = SplitCfg<BN>;
-    constexpr int NS = C::NS;
+    constexpr int NS = C::NS, KS = C::KS;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) uint64_t bars[2 * NS + 2];
@@ -414,9 +477,10 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
     const Waiter drain{&abort_flag, wait_ns > kDrainNs ? wait_ns : kDrainNs};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    const uint32_t base = smem_u32(sm);
     const int tile = blockIdx.x / S;
     const int m0 = (tile % mt) * 128, n0 = (tile / mt) * BN;
-    const int k_lo = (int)((int64_t)ksteps * rank / S), k_hi = (int)((int64_t)ksteps * (rank + 1) / S);
+    const int k_lo = (int)((int64_t)kblocks * rank / S), k_hi = (int)((int64_t)kblocks * (rank + 1) / S);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -436,49 +500,69 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
     bool done = true;                    // the warp's wait completed
 
     if (warp == 0) {
-        if (lane == 0) {
-            bool ok = true;
-            for (int ks = k_lo; ks < k_hi; ++ks) {
-                const int it = ks - k_lo, s = it % NS;
-                if (it >= NS && !(ok = wait(empty(s), (uint32_t)(it / NS - 1) & 1u, E_STAGE))) break;
-                mbar_arrive_tx(full(s), C::STAGE);
-                const uint32_t a = smem_u32(sm + s * C::STAGE), b = a + C::A_BYTES;
-                if constexpr (A_MN) {
-                    tma_load_2d(a, &maps.a, full(s), m0, ks * BK);
-                    tma_load_2d(a + BLK, &maps.a, full(s), m0 + 64, ks * BK);
-                } else {
-                    tma_load_2d(a, &maps.a, full(s), ks * BK, m0);
-                }
-                if constexpr (B_MN) {
+        Ring<NS> ring;
+        bool ok = true;
+        for (int kb = k_lo; kb < k_hi; kb += KS, ring.next()) {
+            const int s = ring.s;
+            if (!(ok = wait.warp(empty(s), ring.parity ^ 1u, E_STAGE))) break;
+            if (elect_one()) {
+                const int nb = k_hi - kb < KS ? k_hi - kb : KS;
+                mbar_arrive_tx(full(s), C::BLOCK * nb);
 #pragma unroll
-                    for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * BLK, &maps.b, full(s), n0 + 64 * j, ks * BK);
-                } else {
-                    tma_load_2d(b, &maps.b, full(s), ks * BK, n0);
+                for (int u = 0; u < KS; ++u) {
+                    if (u >= nb) break;
+                    const uint32_t a = base + s * C::STAGE + u * C::BLOCK, b = a + C::A_BYTES;
+                    const int k = (kb + u) * BK;
+                    if constexpr (A_MN) {
+                        tma_load_2d(a, &maps.a, full(s), m0, k);
+                        tma_load_2d(a + BLK, &maps.a, full(s), m0 + 64, k);
+                    } else {
+                        tma_load_2d(a, &maps.a, full(s), k, m0);
+                    }
+                    if constexpr (B_MN) {
+#pragma unroll
+                        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * BLK, &maps.b, full(s), n0 + 64 * j, k);
+                    } else {
+                        tma_load_2d(b, &maps.b, full(s), k, n0);
+                    }
                 }
             }
-            if (!ok) pause_ns(kLandNs);
+            __syncwarp();
         }
+        if (!ok) pause_ns(kLandNs);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t ID = idesc(128, BN, A_MN, B_MN);
-            bool ok = true;
-            for (int ks = k_lo; ks < k_hi; ++ks) {
-                const int it = ks - k_lo, s = it % NS;
-                if (!(ok = wait(full(s), (uint32_t)(it / NS) & 1u, E_STAGE))) break;
-                tc_fence_after();
-                const uint32_t a = smem_u32(sm + s * C::STAGE), b = a + C::A_BYTES;
+        constexpr uint32_t ID = idesc(128, BN, A_MN, B_MN);
+        const uint64_t da0 = base_desc<A_MN>(base), db0 = base_desc<B_MN>(base + C::A_BYTES);
+        Ring<NS> ring;
+        bool ok = true;
+        for (int kb = k_lo; kb < k_hi; kb += KS, ring.next()) {
+            const int s = ring.s;
+            if (!(ok = wait.warp(full(s), ring.parity, E_STAGE))) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < BK / 16; ++k)
-                    mma_bf16(tm, step_desc<A_MN>(a, k), step_desc<B_MN>(b, k), ID, (it > 0 || k > 0) ? 1u : 0u);
+                for (int u = 0; u < KS; ++u) {
+                    if (kb + u >= k_hi) break;
+                    const uint32_t off = (uint32_t)(s * (C::STAGE >> 4) + u * (C::BLOCK >> 4));
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k)
+                        mma_bf16(tm, da0 + off + k * K16<A_MN>, db0 + off + k * K16<B_MN>, ID,
+                                 (kb > k_lo || u > 0 || k > 0) ? 1u : 0u);
+                }
                 mma_commit(empty(s));
+                if (kb + KS >= k_hi) mma_commit(accf);
             }
-            mma_commit(ok ? accf : drained);
-            if (!ok) drain(drained, 0u, E_DRAIN, false);
+            __syncwarp();
+        }
+        if (!ok) {
+            // every MMA issued so far: TMEM must be idle before it is freed
+            if (elect_one()) mma_commit(drained);
+            drain.warp(drained, 0u, E_DRAIN, false);
         }
         __syncwarp();
     } else {
-        done = __all_sync(0xffffffffu, wait(accf, 0u, E_ACC));
+        done = wait.warp(accf, 0u, E_ACC);
         tc_fence_after();
     }
 
@@ -486,78 +570,71 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
     const int64_t r = (int64_t)m0 + 32 * q + lane;
     const uint32_t tq = tm + ((uint32_t)(32 * q) << 16);
     const float bias = warp >= 2 && ep.bias && r < Mr ? __ldg(ep.bias + r) : 0.f;
-    // the outputs of columns c .. c + n - 1 (n <= 16) from their sums
-    auto emit = [&](int c, int n, float (&v)[16]) {
-        if (r >= Mr) return;
-        if (ep.z) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (j < n && n0 + c + j < Nc) store_elem(ep.z + (n0 + (int64_t)c + j) * Mr + r, v[j] + bias);
-        }
-        with_act(ep.act, [&](auto kind) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (j < n && n0 + c + j < Nc) {
-                    const int64_t at = (n0 + (int64_t)c + j) * Mr + r;
-                    float o = act_value<kind(), true>(v[j] + bias);
-                    if (ep.residual) o += to_f32(__ldg(ep.residual + at));
-                    store_elem(ep.D + at, o);
-                }
-        });
-    };
-    constexpr int HALF = BN / 2, STEP = HALF < 16 ? HALF : 16;      // columns of a warp, and per TMEM load
+    constexpr int HALF = BN / 2;
     if (S == 1) {
+        // a thread owns a row; its stores and those of its warp's other lanes are contiguous
         if (warp >= 2 && done) {
-            for (int c = h * HALF; c < (h + 1) * HALF; c += STEP) {
-                if (n0 + c >= Nc) break;
-                float v[16];
-                if constexpr (STEP == 16) {
-                    tmem_ld16(tq + c, v);
-                } else {
-                    const uint4 lo = tmem_ld4(tq + c), hi = tmem_ld4(tq + c + 4);
-                    v[0] = __uint_as_float(lo.x); v[1] = __uint_as_float(lo.y); v[2] = __uint_as_float(lo.z);
-                    v[3] = __uint_as_float(lo.w); v[4] = __uint_as_float(hi.x); v[5] = __uint_as_float(hi.y);
-                    v[6] = __uint_as_float(hi.z); v[7] = __uint_as_float(hi.w);
+            const int c_lo = h * HALF, c_hi = c_lo + HALF < Nc - n0 ? c_lo + HALF : (int)(Nc - n0);
+            with_act(ep.act, [&](auto kind) {
+#pragma unroll 1
+                for (int c = c_lo; c < c_hi; c += 8) {
+                    float v[8];
+                    tmem_ld8(tq + c, v);
+                    int64_t at = (n0 + (int64_t)c) * Mr + r;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j, at += Mr)
+                        if (c + j < c_hi && r < Mr) {
+                            const float z = v[j] + bias;
+                            if (ep.z) store_elem(ep.z + at, z);
+                            float o = act_value<kind(), true>(z);
+                            if (ep.residual) o += to_f32(__ldg(ep.residual + at));
+                            store_elem(ep.D + at, o);
+                        }
                 }
-                emit(c, STEP, v);
-            }
+            });
         }
     } else {
-        // the partial tile over the stages (their loads have been consumed), [column][128 rows]
+        // The partial tile goes over the stages (their loads have been consumed), [column][128 rows].
+        // In that order CTA r adds up the r-th part of it, four rows of a column per thread: 16-byte
+        // reads of the other CTAs' shared memory, several times the rate of 4-byte ones.
         float* part = reinterpret_cast<float*>(sm);
         if (warp >= 2 && done) {
-            for (int c = h * HALF; c < (h + 1) * HALF; c += STEP) {
-                float v[16];
-                if constexpr (STEP == 16) {
-                    tmem_ld16(tq + c, v);
-                } else {
-                    const uint4 lo = tmem_ld4(tq + c), hi = tmem_ld4(tq + c + 4);
-                    v[0] = __uint_as_float(lo.x); v[1] = __uint_as_float(lo.y); v[2] = __uint_as_float(lo.z);
-                    v[3] = __uint_as_float(lo.w); v[4] = __uint_as_float(hi.x); v[5] = __uint_as_float(hi.y);
-                    v[6] = __uint_as_float(hi.z); v[7] = __uint_as_float(hi.w);
-                }
+#pragma unroll 1
+            for (int c = h * HALF; c < (h + 1) * HALF; c += 8) {
+                float v[8];
+                tmem_ld8(tq + c, v);
 #pragma unroll
-                for (int j = 0; j < STEP; ++j) part[(c + j) * 128 + 32 * q + lane] = v[j];
+                for (int j = 0; j < 8; ++j) part[(c + j) * 128 + 32 * q + lane] = v[j];
             }
         }
         __syncwarp();
         cluster_sync_all();
         if (warp >= 2 && done) {
-            // this CTA's BN / S columns, half of them per warp of a lane quarter
-            const int per = BN / S / 2, c_lo = rank * 2 * per + h * per;
-            for (int c = c_lo; c < c_lo + per; c += 16) {
-                const int n = per < 16 ? per : 16;
-                float v[16];
+            const int share = BN * 32 / S;             // groups of four rows
+            with_act(ep.act, [&](auto kind) {
+#pragma unroll 1
+                for (int i = threadIdx.x - 64; i < share; i += 32 * EPI) {
+                    const int g = rank * share + i, c = g / 32;
+                    const int64_t r4 = (int64_t)m0 + 4 * (g % 32);
+                    if (n0 + c >= Nc || r4 >= Mr) continue;
+                    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+                    for (int p = 0; p < S; ++p) {
+                        const float4 f = ld_cluster_v4(mapa(base + 16 * g, (uint32_t)p));
+                        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+                    }
+                    const int64_t at = (n0 + (int64_t)c) * Mr + r4;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = 0.f;
-                for (int p = 0; p < S; ++p) {
-                    const uint32_t at = mapa(smem_u32(part + c * 128 + 32 * q + lane), (uint32_t)p);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j < n) v[j] += ld_cluster_f32(at + j * 512);
+                    for (int j = 0; j < 4; ++j)
+                        if (r4 + j < Mr) {
+                            const float z = v[j] + (ep.bias ? __ldg(ep.bias + r4 + j) : 0.f);
+                            if (ep.z) store_elem(ep.z + at + j, z);
+                            float o = act_value<kind(), true>(z);
+                            if (ep.residual) o += to_f32(__ldg(ep.residual + at + j));
+                            store_elem(ep.D + at + j, o);
+                        }
                 }
-                emit(c, n, v);
-            }
+            });
         }
         __syncwarp();
         cluster_sync_all();              // no CTA leaves while its partial tile is read
@@ -685,22 +762,69 @@ bool gemm_tc_ok(const GemmArgs& g) {
            g.M < lim && g.N < lim && g.K < lim;
 }
 
+namespace {
+
+// Which kernel runs a product.
+struct Plan {
+    int pair_bn;                         // 256 or 128: the pair kernel; 0: the split kernel
+    int bn, S;                           // of the split kernel
+};
+
+// Up to 64 rows of A, the split kernel with the narrowest MMA N that holds them, and K split until two
+// CTAs per SM stream the other operand.  Above that, the smallest of these times, in us, with kb
+// blocks of 64 along K and w rounds of tiles over the device; measured with the operands in L2 (T from
+// 100 to 8192, K and N from 256 to 16384), each within a fifth of its kernel's time:
+//   pair, 256 x 256   w max(0.30 kb, 2.9)      28 at T = 1024, 4096 -> 4096 (256 x 128: 31, split: 43)
+//   pair, 256 x 128   w max(0.185 kb, 2.0)     8.0 at T = 512, 1024 -> 1024 (256 x 256: 11, split: 9.4)
+//   split by S        w (0.23 kb / S + 3.5) - 3, and 3 more to join the parts
+//                                              17 at T = 333, 8192 -> 1000 with S = 4 (pair: 29)
+Plan plan(const GemmArgs& g, int sms) {
+    Plan p{};
+    const int64_t kb = (g.K + 63) / 64, rows = (g.N + 127) / 128;
+    auto rounds = [](int64_t tiles, int64_t at_once) { return (double)((tiles + at_once - 1) / at_once); };
+    if (g.M <= 64) {
+        p.bn = g.a_mn || g.M > 32 ? 64 : g.M > 16 ? 32 : 16;    // a product over tokens has boxes of 64
+        const int64_t tiles = rows;
+        p.S = 1;
+        while (p.S < 8 && tiles * p.S * 2 <= 2 * sms && kb >= p.S * 4) p.S *= 2;
+        return p;
+    }
+    const int64_t mt = (g.M + 255) / 256;
+    double best = rounds(mt * ((g.N + 255) / 256), sms / 2) * std::max(0.30 * kb, 2.9);
+    p.pair_bn = 256;
+    const double half = rounds(mt * ((g.N + 127) / 128), sms / 2) * std::max(0.185 * kb, 2.0);
+    if (half < best) {
+        best = half;
+        p.pair_bn = 128;
+    }
+    p.bn = 128;
+    for (int S = 1; S <= 8 && kb >= 2 * S - 1; S *= 2) {
+        // clusters at once: a GPC of 16 to 20 SMs holds two clusters of 8
+        const int64_t at_once = S == 8 ? sms * 3 / 32 : sms / S;
+        const double t = rounds(rows * ((g.M + 127) / 128), at_once) * (0.23 * kb / S + 3.5 + (S > 1 ? 3.0 : 0.0)) - 3.0;
+        if (t < best) {
+            best = t;
+            p.pair_bn = 0;
+            p.S = S;
+        }
+    }
+    return p;
+}
+
+}  // namespace
+
 cudaError_t launch_gemm_tc(const GemmArgs& g) {
     DeviceInfo di;
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
-    const int64_t big = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-    if (2 * big >= di.sm_count) return lintc::pair_layout<256>(g, di.sm_count);
-    // a narrow MMA N for few tokens; a product over tokens (rows contiguous) has boxes of 64
-    const int bn = g.a_mn ? (g.M <= 64 ? 64 : 128) : g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
-    const int64_t tiles = ((g.N + 127) / 128) * ((g.M + bn - 1) / bn), steps = (g.K + 63) / 64;
-    int S = 1;
-    while (S < 8 && tiles * S * 2 <= 2 * di.sm_count && steps >= S * 4) S *= 2;
-    switch (bn) {
-        case 16: return lintc::split_layout<16>(g, S);
-        case 32: return lintc::split_layout<32>(g, S);
-        case 64: return lintc::split_layout<64>(g, S);
-        default: return lintc::split_layout<128>(g, S);
+    const Plan p = plan(g, di.sm_count);
+    if (p.pair_bn == 256) return lintc::pair_layout<256>(g, di.sm_count);
+    if (p.pair_bn == 128) return lintc::pair_layout<128>(g, di.sm_count);
+    switch (p.bn) {
+        case 16: return lintc::split_layout<16>(g, p.S);
+        case 32: return lintc::split_layout<32>(g, p.S);
+        case 64: return lintc::split_layout<64>(g, p.S);
+        default: return lintc::split_layout<128>(g, p.S);
     }
 }
 
