@@ -83,6 +83,8 @@ ln_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
     using P = Pack<T, VEC>;
     __shared__ float buf[WARP ? 1 : 64 * R];
     int phase = 0;
+    pdl_launch_next();
+    pdl_wait();
     const int nthr = WARP ? 32 : blockDim.x;
     const int idx = WARP ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t groups = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
@@ -171,6 +173,8 @@ ln_fwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
                                    float* __restrict__ mean_out, float* __restrict__ rstd_out) {
     __shared__ float buf[64];
     int phase = 0;
+    pdl_launch_next();
+    pdl_wait();
     const float inv_d = 1.0f / (float)d;
     for (int64_t row = blockIdx.x; row < Tn; row += gridDim.x) {
         const T* xr = x + row * d;
@@ -205,6 +209,8 @@ ln_bwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
     __shared__ float buf[WARP ? 1 : 64 * 2 * R];
     extern __shared__ float cols[];        // WARP: [2][d] column sums of the block
     int phase = 0;
+    pdl_launch_next();
+    pdl_wait();
     const int nthr = WARP ? 32 : blockDim.x;
     const int idx = WARP ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t groups = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
@@ -325,6 +331,8 @@ ln_bwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
                                    const T* __restrict__ dy, int64_t Tn, int d, T* __restrict__ dx, float* part) {
     __shared__ float buf[64 * 2];
     int phase = 0;
+    pdl_launch_next();
+    pdl_wait();
     const float inv_d = 1.0f / (float)d;
     float* pw = part ? part + (int64_t)blockIdx.x * 2 * d : nullptr;
     for (int64_t row = blockIdx.x; row < Tn; row += gridDim.x) {
@@ -358,6 +366,7 @@ ln_bwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
 __global__ void __launch_bounds__(256)
 ln_cols_kernel(const float* __restrict__ part, int P, int d, float* __restrict__ dw, float* __restrict__ db) {
     __shared__ float sm[8][33];
+    pdl_launch_next();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
@@ -379,12 +388,15 @@ ln_cols_kernel(const float* __restrict__ part, int P, int d, float* __restrict__
 
 bool rows16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-// resident blocks of a kernel on the device, for a grid that walks its rows
+// resident blocks of a kernel on the device, for a grid that walks its rows; not asked where the
+// blocks wanted are no more than the SMs
 template <typename K>
-cudaError_t resident(K kern, int threads, size_t smem, int* blocks) {
+cudaError_t resident(K kern, int threads, size_t smem, int64_t want, int* blocks) {
     DeviceInfo di;
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
+    *blocks = di.sm_count;
+    if (want <= di.sm_count) return cudaSuccess;
     int per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
     *blocks = di.sm_count * (per_sm > 0 ? per_sm : 1);
@@ -396,13 +408,12 @@ cudaError_t fwd(const LnArgs& a) {
     const int chunks = (a.d + VEC - 1) / VEC;
     const int threads = WARP ? 32 * WARPS : ((chunks + NV - 1) / NV + 31) / 32 * 32;
     auto kern = ln_fwd_kernel<T, VEC, NV, R, WARP>;
-    int cap;
-    cudaError_t e = resident(kern, threads, 0, &cap);
-    if (e != cudaSuccess) return e;
     const int64_t want = WARP ? (a.T + WARPS - 1) / WARPS : a.T;
-    kern<<<(unsigned)(want < cap ? want : cap), threads, 0, a.stream>>>(
-        static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
-    return cudaGetLastError();
+    int cap;
+    const cudaError_t e = resident(kern, threads, 0, want, &cap);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)(want < cap ? want : cap)), dim3(threads), 0, a.stream,
+                      static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
 }
 
 template <typename T, int VEC, int NV, int R, bool WARP>
@@ -411,15 +422,14 @@ cudaError_t bwd(const LnArgs& a, int* blocks) {
     const int threads = WARP ? 32 * WARPS : ((chunks + NV - 1) / NV + 31) / 32 * 32;
     const size_t smem = WARP ? (size_t)2 * a.d * 4 : 0;
     auto kern = ln_bwd_kernel<T, VEC, NV, R, WARP>;
+    const int64_t want = WARP ? (a.T + WARPS - 1) / WARPS : a.T;
     int cap;
-    cudaError_t e = resident(kern, threads, smem, &cap);
+    const cudaError_t e = resident(kern, threads, smem, want, &cap);
     if (e != cudaSuccess) return e;
     if (cap > BWD_BLOCKS) cap = BWD_BLOCKS;
-    const int64_t want = WARP ? (a.T + WARPS - 1) / WARPS : a.T;
     *blocks = (int)(want < cap ? want : cap);
-    kern<<<*blocks, threads, smem, a.stream>>>(static_cast<const T*>(a.x), a.w, a.mean, a.rstd,
-                                               static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3((unsigned)*blocks), dim3(threads), smem, a.stream, static_cast<const T*>(a.x), a.w,
+                      a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part);
 }
 
 // The layout of a row by its length in vectors: a warp up to 4 vectors per lane, a block with 2
@@ -442,11 +452,10 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
         if (a.d <= 8192) return fwd<T, 1, 16, 1, false>(a);
     }
     int cap;
-    cudaError_t e = resident(ln_fwd_long_kernel<T>, 1024, 0, &cap);
+    cudaError_t e = resident(ln_fwd_long_kernel<T>, 1024, 0, a.T, &cap);
     if (e != cudaSuccess) return e;
-    ln_fwd_long_kernel<T><<<(unsigned)(a.T < cap ? a.T : cap), 1024, 0, a.stream>>>(
-        static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
-    return cudaGetLastError();
+    return launch_pdl(ln_fwd_long_kernel<T>, dim3((unsigned)(a.T < cap ? a.T : cap)), dim3(1024), 0, a.stream,
+                      static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
 }
 
 template <typename T>
@@ -466,14 +475,13 @@ cudaError_t bwd_t(const LnArgs& a, int* blocks) {
         if (a.d <= 8192) return bwd<T, 1, 16, 1, false>(a, blocks);
     }
     int cap;
-    cudaError_t e = resident(ln_bwd_long_kernel<T>, 1024, 0, &cap);
+    cudaError_t e = resident(ln_bwd_long_kernel<T>, 1024, 0, a.T, &cap);
     if (e != cudaSuccess) return e;
     if (cap > BWD_BLOCKS) cap = BWD_BLOCKS;
     *blocks = (int)(a.T < cap ? a.T : cap);
-    ln_bwd_long_kernel<T><<<*blocks, 1024, 0, a.stream>>>(static_cast<const T*>(a.x), a.w, a.mean, a.rstd,
-                                                          static_cast<const T*>(a.dy), a.T, a.d,
-                                                          static_cast<T*>(a.dx), a.part);
-    return cudaGetLastError();
+    return launch_pdl(ln_bwd_long_kernel<T>, dim3((unsigned)*blocks), dim3(1024), 0, a.stream,
+                      static_cast<const T*>(a.x), a.w, a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d,
+                      static_cast<T*>(a.dx), a.part);
 }
 
 }  // namespace

@@ -49,6 +49,8 @@ dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, 
           int64_t ld, float* __restrict__ part) {
     constexpr int U = 4;
     __shared__ float sm[DZ_ROWS][DZ_COLS * VEC + 1];
+    pdl_launch_next();
+    pdl_wait();
     const int tx = threadIdx.x % DZ_COLS, ty = threadIdx.x / DZ_COLS;
     const int64_t c = ((int64_t)blockIdx.x * DZ_COLS + tx) * VEC;
     const int64_t t0 = (int64_t)blockIdx.y * run, t1 = t0 + run < Tn ? t0 + run : Tn;
@@ -102,6 +104,7 @@ dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, 
 __global__ void __launch_bounds__(256)
 sum_rows_kernel(const float* __restrict__ part, int64_t P, int N, float* __restrict__ out) {
     __shared__ float sm[8][33];
+    pdl_launch_next();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
@@ -118,12 +121,13 @@ sum_rows_kernel(const float* __restrict__ part, int64_t P, int N, float* __restr
 }
 
 template <typename T, int VEC, bool SHIFT>
-void start_dz(const LinearArgs& a, void* dz, int64_t ld, int64_t run, int64_t rows, float* sums) {
+cudaError_t start_dz(const LinearArgs& a, void* dz, int64_t ld, int64_t run, int64_t rows, float* sums) {
     const int cols = DZ_COLS * VEC;
     const dim3 grid((unsigned)((a.N + (int64_t)cols - 1) / cols), (unsigned)rows);
+    cudaError_t e = cudaSuccess;
     auto go = [&](auto kern) {
-        kern<<<grid, DZ_COLS * DZ_ROWS, 0, a.stream>>>(static_cast<const T*>(a.dy), static_cast<const T*>(a.z), a.T,
-                                                       a.N, run, static_cast<T*>(dz), ld, sums);
+        e = launch_pdl(kern, grid, dim3(DZ_COLS * DZ_ROWS), 0, a.stream, static_cast<const T*>(a.dy),
+                       static_cast<const T*>(a.z), a.T, a.N, run, static_cast<T*>(dz), ld, sums);
     };
     switch (a.act) {
         case ACT_RELU: go(dz_kernel<T, VEC, ACT_RELU, SHIFT>); break;
@@ -132,6 +136,7 @@ void start_dz(const LinearArgs& a, void* dz, int64_t ld, int64_t run, int64_t ro
         case ACT_SILU: go(dz_kernel<T, VEC, ACT_SILU, SHIFT>); break;
         default: go(dz_kernel<T, VEC, ACT_NONE, SHIFT>); break;
     }
+    return e;
 }
 
 template <typename T>
@@ -141,13 +146,13 @@ cudaError_t launch_dz(const LinearArgs& a, void* dz, int64_t ld, float* part) {
     const int64_t run = ((a.T + runs - 1) / runs + DZ_ROWS - 1) / DZ_ROWS * DZ_ROWS;
     const int64_t rows = (a.T + run - 1) / run;      // runs that hold tokens
     float* sums = a.dbias ? (rows == 1 ? a.dbias : part) : nullptr;
+    cudaError_t e;
     if (a.N % V == 0 && (uintptr_t)a.dy % 16 == 0 && (uintptr_t)a.z % 16 == 0)
-        start_dz<T, V, false>(a, dz, ld, run, rows, sums);
+        e = start_dz<T, V, false>(a, dz, ld, run, rows, sums);
     else if constexpr (sizeof(T) == 2)
-        start_dz<T, V, true>(a, dz, ld, run, rows, sums);
+        e = start_dz<T, V, true>(a, dz, ld, run, rows, sums);
     else
-        start_dz<T, 1, false>(a, dz, ld, run, rows, sums);
-    cudaError_t e = cudaGetLastError();
+        e = start_dz<T, 1, false>(a, dz, ld, run, rows, sums);
     if (e == cudaSuccess && a.dbias && rows > 1)
         e = launch_pdl(sum_rows_kernel, dim3((unsigned)((a.N + (int64_t)31) / 32)), dim3(256), 0, a.stream, part,
                        rows, a.N, a.dbias);
@@ -165,6 +170,8 @@ struct PadJob {
 
 __global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ PadJob a, const __grid_constant__ PadJob b) {
     const PadJob& j = blockIdx.y ? b : a;
+    pdl_launch_next();
+    pdl_wait();
     const int64_t per = j.ld / 8, total = j.rows * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / per, c = (i - row * per) * 8;
@@ -175,8 +182,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ P
 cudaError_t pad_rows(const PadJob& a, const PadJob& b, cudaStream_t s) {
     const int64_t n = std::max(a.rows * a.ld, b.rows * b.ld) / 8;
     const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 8 * 148);
-    pad_rows_kernel<<<dim3(blocks, b.rows ? 2 : 1), 256, 0, s>>>(a, b);
-    return cudaGetLastError();
+    return launch_pdl(pad_rows_kernel, dim3(blocks, b.rows ? 2 : 1), dim3(256), 0, s, a, b);
 }
 
 int64_t padded(int64_t cols) { return (cols + 7) / 8 * 8; }

@@ -29,6 +29,9 @@ gemm_kernel(const T* __restrict__ A, const T* __restrict__ B, int64_t lda, int64
     const int64_t mt = (M + BM - 1) / BM;
     const int64_t m0 = (int64_t)(blockIdx.x % mt) * BM, n0 = (int64_t)(blockIdx.x / mt) * BM;
 
+    pdl_launch_next();
+    pdl_wait();
+
     float acc[TM][TM] = {};
     float ra[LD], rb[LD];
     // element j of this thread: (row, k) within the tile, consecutive threads along the contiguous index
@@ -102,10 +105,9 @@ cudaError_t launch(const GemmArgs& g) {
     constexpr int BM = 16 * TM;
     const int64_t tiles = ((g.M + BM - 1) / BM) * ((g.N + BM - 1) / BM);
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    gemm_kernel<T, TM, A_MN, B_MN><<<(unsigned)tiles, THREADS, 0, g.stream>>>(
-        static_cast<const T*>(g.A), static_cast<const T*>(g.B), g.lda, g.ldb, g.M, g.N, g.K, g.bias,
-        static_cast<const T*>(g.residual), (int)g.act, static_cast<T*>(g.D), static_cast<T*>(g.z));
-    return cudaGetLastError();
+    return launch_pdl(gemm_kernel<T, TM, A_MN, B_MN>, dim3((unsigned)tiles), dim3(THREADS), 0, g.stream,
+                      static_cast<const T*>(g.A), static_cast<const T*>(g.B), g.lda, g.ldb, g.M, g.N, g.K, g.bias,
+                      static_cast<const T*>(g.residual), (int)g.act, static_cast<T*>(g.D), static_cast<T*>(g.z));
 }
 
 template <typename T, bool A_MN, bool B_MN>

@@ -255,6 +255,10 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
+    // The next kernel may set itself up from here on, not before: a CTA of it that took this one's
+    // TMEM would wait for this kernel's end.  What the previous one wrote is there after the wait.
+    pdl_launch_next();
+    pdl_wait();
     const uint32_t tm = tmem_slot;
     const int64_t tiles = (int64_t)mt * nt;
     const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
@@ -482,21 +486,32 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
     const int m0 = (tile % mt) * 128, n0 = (tile / mt) * BN;
     const int k_lo = (int)((int64_t)kblocks * rank / S), k_hi = (int)((int64_t)kblocks * (rank + 1) / S);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+    // Warp 0 sets up the barriers and goes on to load at once; the others meet after TMEM is there.
+    // As in the pair kernel, the next kernel may start once this CTA holds its TMEM.
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int s = 0; s < NS; ++s) {
+                mbar_init(full(s), 1);
+                mbar_init(empty(s), 1);
+            }
+            mbar_init(accf, 1);
+            mbar_init(drained, 1);
+            abort_flag = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-        mbar_init(accf, 1);
-        mbar_init(drained, 1);
-        abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncwarp();
+        asm volatile("bar.arrive 1, %0;" :: "n"(THREADS) : "memory");
+    } else {
+        if (warp == 1) {
+            tmem_alloc(smem_u32(&tmem_slot), C::TMEM_COLS);
+            pdl_launch_next();
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" :: "n"(THREADS) : "memory");
+        tc_fence_after();
     }
-    if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), C::TMEM_COLS);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = tmem_slot;
+    const uint32_t tm = warp == 0 ? 0u : tmem_slot;
+    pdl_wait();                          // what the previous kernel wrote is there
     bool done = true;                    // the warp's wait completed
 
     if (warp == 0) {
@@ -707,9 +722,8 @@ cudaError_t pair_launch(const GemmArgs& g, int sms) {
     const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + BN - 1) / BN);
     const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    kern<<<grid, THREADS, C::SMEM, g.stream>>>(maps, epilogue_of(g), g.M, g.N, (int)((g.K + BK - 1) / BK), mt, nt,
-                                               g_wait_ns.load());
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(grid), dim3(THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of(g), g.M, g.N,
+                      (int)((g.K + BK - 1) / BK), mt, nt, g_wait_ns.load());
 }
 
 template <int BN>
@@ -735,12 +749,14 @@ cudaError_t split_launch(const GemmArgs& g, int S) {
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = g.stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)S;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)S;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = S > 1 ? 1 : 0;
+    cfg.numAttrs = S > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, maps, epilogue_of(g), g.N, g.M, (int)((g.K + BK - 1) / BK), mt, S,
                               g_wait_ns.load());
 }
