@@ -422,7 +422,8 @@ mhc_status mhc_amax_gain(const float* H_layers, int L, int64_t T, int n, float* 
  * time (1 s each); a wait that expires makes the kernel stop early, leaving its outputs
  * incomplete, and sets a bit here naming the wait: bits 0-15 the cluster pre kernel, 16-23
  * the two-pass pre kernels, 24-28 the tensor-core dX / dphi step of mhc_backward, 29-31 the
- * tensor-core products of mhc_linear and mhc_linear_backward.  *code = 0
+ * sub-layer operators (29 their loads: the layer norms' and the products'; 30 and 31 the
+ * products' accumulators and drains).  *code = 0
  * means every wait of every launch since the last read completed.  Blocks until prior work on the legacy default
  * stream (and streams that synchronise with it) has finished.  No counterpart on the
  * pages: this is the library's failure report.

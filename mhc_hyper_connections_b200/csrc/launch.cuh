@@ -174,6 +174,7 @@ struct LnArgs {
 int64_t layer_norm_part_floats(int64_t T, int d);
 cudaError_t launch_layer_norm(const LnArgs& a);
 cudaError_t launch_layer_norm_backward(const LnArgs& a);
+cudaError_t layer_norm_status(unsigned* out, bool clear);
 
 // The linear product with its epilogue, forward and backward (linear.cu).
 enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };

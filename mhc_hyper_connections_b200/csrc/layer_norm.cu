@@ -13,18 +13,30 @@
 //
 // A row belongs to one warp (WARP, rows of up to 4 vectors per lane) or to one thread block.  A
 // thread owns the same NV vectors of VEC columns in every row it sees, so w and b are loaded once
-// and the backward's column sums stay in registers until the thread's last row.  A group takes R
-// rows at a time: their loads are in flight together and they share each reduction's barrier.
+// and the backward's column sums stay in registers until the thread's last row.
+//   * ring kernels, for aligned rows and more of them than SMs: a warp of its own brings the next rows
+//     into a ring in shared memory by bulk copies, so the loads in flight do not depend on what the
+//     other warps are doing (without it a block's reductions and stores left HBM idle: 86 us forward at
+//     T = 16384, d = 4096, bf16);
+//   * register kernels, for few rows (latency counts: one vector per thread, no ring to set up) and
+//     for rows that are not 16-byte aligned (one element at a time);
+//   * long kernels, for rows beyond the registers of a block: three walks over the row.
 // Column sums are added up in a fixed order: over a group's rows, over a block's warps in shared
 // memory, and over the blocks by a second kernel that reads one fp32 row pair per block.
 #include "common.cuh"
 #include "launch.cuh"
+#include "tc_ptx.cuh"
 
 namespace mhc {
+
+// 1 once a bounded wait of the ring kernels expired (mhc_device_status).
+__device__ unsigned int g_layer_norm_status;
+
 namespace {
 
-// blocks that write column-sum rows for the second kernel: three per SM of a 148-SM device
-constexpr int BWD_BLOCKS = 444;
+// blocks that write column-sum rows for the second kernel: two per SM of a 148-SM device, and up to
+// eight where rows are short (T = 16384, d = 1024, bf16: 39 us with two)
+int bwd_blocks(int d) { return d >= 4096 ? 296 : d <= 1024 ? 1184 : 296 * 4096 / d; }
 constexpr int WARPS = 8;               // warps per block where a row belongs to a warp
 
 // VEC elements as they lie in memory: 16 bytes, or one element where rows are not 16-byte aligned
@@ -45,24 +57,25 @@ template <typename T, int VEC> struct Pack {
     __device__ __forceinline__ static void store(T* p, const float* f) { st_v4(p, Vec16<T>::pack(f)); }
 };
 
-// Sum R values over the group (a warp, or the block); every thread gets the sums.  The block form
-// alternates between two buffers, so one barrier per call is enough: a buffer is written again
-// only after every thread has passed the barrier of the call in between.
-template <int R, bool WARP>
-__device__ __forceinline__ void group_sum(float (&v)[R], float* buf, int& phase) {
+// Sum R values over the group (G lanes of a warp; G = 0: the first nthr threads of the block); every
+// thread of it gets the sums.  The block form alternates between two buffers, so one barrier per call
+// is enough: a buffer is written again only after every thread has passed the barrier of the call in
+// between.
+template <int R, int G>
+__device__ __forceinline__ void group_sum(float (&v)[R], float* buf, int& phase, int nthr) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = (G ? G : 32) / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
-    if constexpr (!WARP) {
+    if constexpr (G == 0) {
         float* b = buf + phase * 32 * R;
         phase ^= 1;
-        const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+        const int warp = threadIdx.x >> 5, nw = nthr >> 5;
         if ((threadIdx.x & 31) == 0) {
 #pragma unroll
             for (int r = 0; r < R; ++r) b[warp * R + r] = v[r];
         }
-        __syncthreads();
+        asm volatile("bar.sync 1, %0;" :: "r"(nthr) : "memory");
 #pragma unroll
         for (int r = 0; r < R; ++r) v[r] = 0.f;
         for (int w = 0; w < nw; ++w)
@@ -125,7 +138,7 @@ ln_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
                 for (int e = 0; e < VEC; ++e) s[r] += f[e];
             }
         }
-        group_sum<R, WARP>(s, buf, phase);
+        group_sum<R, WARP ? 32 : 0>(s, buf, phase, nthr);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             mean[r] = s[r] * inv_d;
@@ -142,7 +155,7 @@ ln_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
                 }
             }
         }
-        group_sum<R, WARP>(s, buf, phase);
+        group_sum<R, WARP ? 32 : 0>(s, buf, phase, nthr);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = row0 + r * groups;
@@ -180,14 +193,14 @@ ln_fwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
         const T* xr = x + row * d;
         float s[1] = {0.f};
         for (int c = threadIdx.x; c < d; c += blockDim.x) s[0] += to_f32(__ldg(xr + c));
-        group_sum<1, false>(s, buf, phase);
+        group_sum<1, 0>(s, buf, phase, blockDim.x);
         const float mean = s[0] * inv_d;
         s[0] = 0.f;
         for (int c = threadIdx.x; c < d; c += blockDim.x) {
             const float v = to_f32(__ldg(xr + c)) - mean;
             s[0] = fmaf(v, v, s[0]);
         }
-        group_sum<1, false>(s, buf, phase);
+        group_sum<1, 0>(s, buf, phase, blockDim.x);
         const float rstd = 1.0f / sqrtf(fmaf(s[0], inv_d, eps));
         for (int c = threadIdx.x; c < d; c += blockDim.x)
             store_elem(y + row * d + c, fmaf((to_f32(__ldg(xr + c)) - mean) * rstd, w ? __ldg(w + c) : 1.f,
@@ -265,7 +278,7 @@ ln_bwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
             }
         }
         if (!dx) continue;
-        group_sum<2 * R, WARP>(sums, buf, phase);
+        group_sum<2 * R, WARP ? 32 : 0>(sums, buf, phase, nthr);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = row0 + r * groups;
@@ -352,7 +365,7 @@ ln_bwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
             }
         }
         if (!dx) continue;
-        group_sum<2, false>(s, buf, phase);
+        group_sum<2, 0>(s, buf, phase, blockDim.x);
         const float a = s[0] * inv_d, k = s[1] * inv_d;
         for (int c = threadIdx.x; c < d; c += blockDim.x) {
             const float xh = (to_f32(__ldg(xr + c)) - mu) * rs;
@@ -361,23 +374,524 @@ ln_bwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
     }
 }
 
-// out[c] = sum over the P blocks of part[p][c], c < 2 d: a block takes 32 columns, its 8 warps a
-// strided share of the rows each, added in a fixed order
-__global__ void __launch_bounds__(256)
+// ---- ring kernels
+
+constexpr int MAX_SLOTS = 8;
+constexpr int WARP_SLOTS = 4;            // of a warp's own ring
+constexpr unsigned long long kRingWaitNs = 1000000000ull;    // 1 s per wait
+constexpr unsigned long long kRingLandNs = 2000000ull;       // after a failed wait: copies in flight land
+
+// A wait that expires sets the status word and the block's abort flag; after it no wait blocks, the
+// loops run out and the outputs are incomplete.
+__device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    for (int i = 0; i < 256; ++i) {
+        if (ptx::mbar_try(bar, parity)) return true;
+        if (*abort_flag) return false;
+    }
+    const uint64_t t0 = ptx::gtimer();
+    while (true) {
+        if (ptx::mbar_try(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (ptx::gtimer() - t0 > kRingWaitNs) {
+            atomicOr(&g_layer_norm_status, 1u);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ void land() {
+    const uint64_t t0 = ptx::gtimer();
+    while (ptx::gtimer() - t0 < kRingLandNs) __nanosleep(1000);
+}
+
+// A ring of slots filled by the producer warp.
+struct Ring {
+    uint64_t* bars;                      // [2 MAX_SLOTS]: full, empty
+    volatile int* abort_flag;
+    int slots;
+    int s = 0;
+    uint32_t parity = 0;
+
+    __device__ __forceinline__ uint32_t full() const { return ptx::smem_u32(bars + s); }
+    __device__ __forceinline__ uint32_t empty() const { return ptx::smem_u32(bars + MAX_SLOTS + s); }
+    __device__ __forceinline__ void next() {
+        if (++s == slots) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t par) const { return wait_until(bar, par, abort_flag); }
+};
+
+// set up by thread 0; the caller synchronises the block
+__device__ __forceinline__ void ring_init(uint64_t* bars, int* abort_flag, int slots, int readers) {
+    for (int i = 0; i < slots; ++i) {
+        ptx::mbar_init(ptx::smem_u32(bars + i), 1);
+        ptx::mbar_init(ptx::smem_u32(bars + MAX_SLOTS + i), readers);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// The producer warp's loop: NT tensors' rows of each of the block's batches, side by side in a slot
+template <int NT>
+__device__ __forceinline__ void ring_produce(Ring ring, unsigned char* smem, const unsigned char* const (&src)[NT],
+                                             int64_t Tn, int B, int64_t row_bytes, int64_t batches) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+        for (int64_t i = blockIdx.x; i < batches; i += gridDim.x, ring.next()) {
+            if (!(ok = ring.wait(ring.empty(), ring.parity ^ 1u))) break;
+            const int64_t row = i * B;
+            const uint32_t bytes = (uint32_t)((Tn - row < B ? Tn - row : B) * row_bytes);
+            ptx::mbar_arrive_tx(ring.full(), NT * bytes);
+            const uint32_t dst = ptx::smem_u32(smem) + (uint32_t)(ring.s * NT * B * row_bytes);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                ptx::bulk_g2s(dst + (uint32_t)(t * B * row_bytes), src[t] + row * row_bytes, bytes, ring.full());
+        }
+        if (!ok) land();
+    }
+    __syncwarp();
+}
+
+// A 16-byte vector as fp32 pairs, and back: the arithmetic below is in pairs, which halves its
+// instructions (at d = 4096 the forward kernel issued more than it loaded without)
+__device__ __forceinline__ void pairs_of(uint4 v, float2 (&f)[4]) {
+    f[0] = bf16x2_to_f32x2(v.x); f[1] = bf16x2_to_f32x2(v.y);
+    f[2] = bf16x2_to_f32x2(v.z); f[3] = bf16x2_to_f32x2(v.w);
+}
+__device__ __forceinline__ void pairs_of(uint4 v, float2 (&f)[2]) {
+    f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ uint4 vector_of(const float2 (&f)[4]) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
+}
+__device__ __forceinline__ uint4 vector_of(const float2 (&f)[2]) {
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                      __float_as_uint(f[1].y));
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// w (or b) of a thread's NV vectors of columns, or `none` where the caller gave no array.  In registers:
+// re-read from L1 for every row (32-byte pieces per thread) they took longer than the row itself.
+template <int NV, int HV>
+__device__ __forceinline__ void load_columns(const float* __restrict__ p, int d, int nthr, int idx, float none,
+                                             float2 (&f)[NV][HV]) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * nthr + idx) * 2 * HV;
+#pragma unroll
+        for (int e = 0; e < HV; ++e)
+            f[v][e] = p && c < d ? make_float2(__ldg(p + c + 2 * e), __ldg(p + c + 2 * e + 1)) : both(none);
+    }
+}
+
+// Rows belong to groups of G lanes (G = 8, 16, 32), or to the block (G = 0).  A group takes R rows at
+// a time, NV 16-byte vectors per thread and row; a slot holds the B rows that the block takes at a time.
+// TH: the most threads that share a row and its registers.
+template <typename T, int NV, int R, int G, int TH>
+__global__ void __launch_bounds__(TH + 32)
+ln_fwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int64_t Tn, int d,
+                   float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots) {
+    constexpr int VEC = Vec16<T>::VEC, HV = VEC / 2;
+    constexpr int B = G ? WARPS * (32 / (G ? G : 32)) * R : R;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ __align__(8) uint64_t bars[2 * MAX_SLOTS];
+    __shared__ int abort_flag;
+    __shared__ __align__(16) float buf[G ? 1 : 64 * R];
+    int phase = 0;
+    const int consumers = blockDim.x - 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) ring_init(bars, &abort_flag, slots, consumers >> 5);
+    __syncthreads();
+    pdl_launch_next();
+    pdl_wait();
+    Ring ring{bars, &abort_flag, slots};
+    const int64_t batches = (Tn + B - 1) / B, row_bytes = (int64_t)d * sizeof(T);
+    if (warp == consumers >> 5) {
+        const unsigned char* const src[1] = {reinterpret_cast<const unsigned char*>(x)};
+        ring_produce<1>(ring, smem, src, Tn, B, row_bytes, batches);
+        return;
+    }
+    const int nthr = G ? G : consumers, idx = G ? lane % (G ? G : 32) : threadIdx.x;
+    const int first = G ? (threadIdx.x / (G ? G : 32)) * R : 0;        // the group's first row of a batch
+    const float inv_d = 1.0f / (float)d;
+    float2 wv[NV][HV], bv[NV][HV];
+    load_columns<NV, HV>(w, d, nthr, idx, 1.f, wv);
+    load_columns<NV, HV>(b, d, nthr, idx, 0.f, bv);
+    for (int64_t i = blockIdx.x; i < batches; i += gridDim.x, ring.next()) {
+        ring.wait(ring.full(), ring.parity);
+        const T* rows = reinterpret_cast<const T*>(smem + (int64_t)ring.s * B * row_bytes) + (int64_t)first * d;
+        // rows past Tn hold what the slot held before; nothing of them is stored
+        uint4 raw[R][NV];
+        float s[R], mean[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float2 acc = both(0.f);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * nthr + idx) * VEC;
+                raw[r][v] = c < d ? *reinterpret_cast<const uint4*>(rows + (int64_t)r * d + c) : make_uint4(0, 0, 0, 0);
+                float2 f[HV];
+                pairs_of(raw[r][v], f);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) acc = __fadd2_rn(acc, f[e]);
+            }
+            s[r] = acc.x + acc.y;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ring.empty());                 // the slot is in registers
+        group_sum<R, G>(s, buf, phase, nthr);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = s[r] * inv_d;
+            float2 acc = both(0.f);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if ((v * nthr + idx) * VEC >= d) continue;
+                float2 f[HV];
+                pairs_of(raw[r][v], f);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) {
+                    const float2 c = __fadd2_rn(f[e], both(-mean[r]));
+                    acc = __ffma2_rn(c, c, acc);
+                }
+            }
+            s[r] = acc.x + acc.y;
+        }
+        group_sum<R, G>(s, buf, phase, nthr);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = i * B + first + r;
+            s[r] = 1.0f / sqrtf(fmaf(s[r], inv_d, eps));               // rstd
+            if (idx == 0 && mean_out && row < Tn) {
+                mean_out[row] = mean[r];
+                rstd_out[row] = s[r];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * nthr + idx) * VEC;
+            if (c >= d) continue;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t row = i * B + first + r;
+                if (row >= Tn) break;
+                float2 f[HV];
+                pairs_of(raw[r][v], f);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) {
+                    const float2 xh = __fmul2_rn(__fadd2_rn(f[e], both(-mean[r])), both(s[r]));
+                    f[e] = __ffma2_rn(xh, wv[v][e], bv[v][e]);
+                }
+                st_v4(y + row * d + c, vector_of(f));
+            }
+        }
+    }
+}
+
+// Forward, a row per warp in NV vectors per lane, with w and b in shared memory.  No barriers: the rows
+// of an SM's warps are at different points, so loads, reductions and stores overlap, and each warp has
+// a ring of its own that it refills as soon as a row is in registers.  The 32-byte pieces of w and b
+// that go with a bf16 vector are stored as two planes of 16 bytes per lane, which reads without bank
+// conflicts.
+// blocks of 256 threads per SM, as many as the registers of a row per warp allow
+template <int NV> constexpr int WARP_BLOCKS = NV > 10 ? 1 : NV > 8 ? 2 : NV > 4 ? 3 : 4;
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(256, WARP_BLOCKS<NV>)
+ln_fwd_warp_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int64_t Tn, int d,
+                   float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots) {
+    constexpr int TH = 256;
+    constexpr int VEC = Vec16<T>::VEC, HV = VEC / 2, PL = VEC / 4;
+    extern __shared__ float4 wb[];      // [w, b][NV][PL][32], then the warps' slots
+    __shared__ __align__(8) uint64_t bars[TH / 32][WARP_SLOTS];
+    __shared__ int abort_flag;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x < TH / 32 * WARP_SLOTS) ptx::mbar_init(ptx::smem_u32(&bars[0][0] + threadIdx.x), 1);
+    if (threadIdx.x == 0) abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncthreads();
+    pdl_launch_next();
+    pdl_wait();
+    const int row_bytes = d * (int)sizeof(T);
+    const int64_t warps = (int64_t)gridDim.x * (TH / 32);
+    int64_t row = (int64_t)warp * gridDim.x + blockIdx.x;      // the last, partial round goes to all blocks
+    unsigned char* ring = reinterpret_cast<unsigned char*>(wb + 2 * NV * PL * 32) + (size_t)warp * slots * row_bytes;
+    auto load = [&](int64_t r, int s) {
+        const uint32_t bar = ptx::smem_u32(&bars[warp][s]);
+        ptx::mbar_arrive_tx(bar, row_bytes);
+        ptx::bulk_g2s(ptx::smem_u32(ring) + s * row_bytes, x + r * d, row_bytes, bar);
+    };
+    if (lane == 0)
+        for (int s = 0; s < slots; ++s)
+            if (row + s * warps < Tn) load(row + s * warps, s);
+    bool ok = true;
+    int slot = 0;
+    uint32_t parity = 0;
+    auto four = [&](const float* p, int c, float none) {
+        if (!p || c >= d) return make_float4(none, none, none, none);
+        if ((uintptr_t)p % 16 == 0) return __ldg(reinterpret_cast<const float4*>(p + c));
+        return make_float4(__ldg(p + c), __ldg(p + c + 1), __ldg(p + c + 2), __ldg(p + c + 3));
+    };
+#pragma unroll 2
+    for (int i = threadIdx.x; i < NV * 32 * PL; i += TH) {
+        const int at = (i / (32 * PL) * PL + i % PL) * 32 + i / PL % 32;
+        wb[at] = four(w, 4 * i, 1.f);
+        wb[NV * PL * 32 + at] = four(b, 4 * i, 0.f);
+    }
+    __syncthreads();
+    const float inv_d = 1.0f / (float)d;
+    for (; row < Tn; row += warps) {
+        ok = wait_until(ptx::smem_u32(&bars[warp][slot]), parity, &abort_flag) && ok;
+        uint4 raw[NV];
+        const T* xr = reinterpret_cast<const T*>(ring + (size_t)slot * row_bytes) + lane * VEC;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            raw[v] = (v * 32 + lane) * VEC < d ? *reinterpret_cast<const uint4*>(xr + v * 32 * VEC)
+                                               : make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        if (lane == 0 && row + slots * warps < Tn) load(row + slots * warps, slot);
+        if (++slot == slots) {
+            slot = 0;
+            parity ^= 1u;
+        }
+        float2 a0 = both(0.f), a1 = both(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float2 f[HV];
+            pairs_of(raw[v], f);
+#pragma unroll
+            for (int e = 0; e < HV; e += 2) {
+                a0 = __fadd2_rn(a0, f[e]);
+                a1 = __fadd2_rn(a1, f[e + 1]);
+            }
+        }
+        float s = (a0.x + a0.y) + (a1.x + a1.y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float mean = s * inv_d;
+        a0 = a1 = both(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if ((v * 32 + lane) * VEC >= d) continue;
+            float2 f[HV];
+            pairs_of(raw[v], f);
+#pragma unroll
+            for (int e = 0; e < HV; e += 2) {
+                const float2 c0 = __fadd2_rn(f[e], both(-mean)), c1 = __fadd2_rn(f[e + 1], both(-mean));
+                a0 = __ffma2_rn(c0, c0, a0);
+                a1 = __ffma2_rn(c1, c1, a1);
+            }
+        }
+        s = (a0.x + a0.y) + (a1.x + a1.y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float rstd = 1.0f / sqrtf(fmaf(s, inv_d, eps));
+        T* yr = y + row * d + lane * VEC;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float2 f[HV];
+            pairs_of(raw[v], f);
+#pragma unroll
+            for (int h = 0; h < PL; ++h) {
+                const float4 wq = wb[(v * PL + h) * 32 + lane], bq = wb[((NV + v) * PL + h) * 32 + lane];
+                const float2 x0 = __fmul2_rn(__fadd2_rn(f[2 * h], both(-mean)), both(rstd));
+                const float2 x1 = __fmul2_rn(__fadd2_rn(f[2 * h + 1], both(-mean)), both(rstd));
+                f[2 * h] = __ffma2_rn(x0, make_float2(wq.x, wq.y), make_float2(bq.x, bq.y));
+                f[2 * h + 1] = __ffma2_rn(x1, make_float2(wq.z, wq.w), make_float2(bq.z, bq.w));
+            }
+            if ((v * 32 + lane) * VEC < d) st_v4(yr + v * 32 * VEC, vector_of(f));
+        }
+        if (lane == 0 && mean_out) {
+            mean_out[row] = mean;
+            rstd_out[row] = rstd;
+        }
+    }
+    if (!ok) land();
+}
+
+// the same; a slot holds B rows of x, then B rows of dy
+template <typename T, int NV, int R, int G, int TH>
+__global__ void __launch_bounds__(TH + 32, 1)
+ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
+                   const float* __restrict__ rstd, const T* __restrict__ dy, int64_t Tn, int d, T* __restrict__ dx,
+                   float* __restrict__ part, int slots) {
+    constexpr int VEC = Vec16<T>::VEC, HV = VEC / 2;
+    constexpr int GROUPS = G ? WARPS * (32 / (G ? G : 32)) : 1, B = GROUPS * R;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ __align__(8) uint64_t bars[2 * MAX_SLOTS];
+    __shared__ int abort_flag;
+    __shared__ __align__(16) float buf[G ? 1 : 128 * R];
+    int phase = 0;
+    const int consumers = blockDim.x - 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) ring_init(bars, &abort_flag, slots, consumers >> 5);
+    __syncthreads();
+    pdl_launch_next();
+    pdl_wait();
+    Ring ring{bars, &abort_flag, slots};
+    const int64_t batches = (Tn + B - 1) / B, row_bytes = (int64_t)d * sizeof(T);
+    if (warp == consumers >> 5) {
+        const unsigned char* const src[2] = {reinterpret_cast<const unsigned char*>(x),
+                                             reinterpret_cast<const unsigned char*>(dy)};
+        ring_produce<2>(ring, smem, src, Tn, B, row_bytes, batches);
+        return;
+    }
+    const int nthr = G ? G : consumers, idx = G ? lane % (G ? G : 32) : threadIdx.x;
+    const int group = G ? threadIdx.x / (G ? G : 32) : 0, first = group * R;
+    const float inv_d = 1.0f / (float)d;
+    float2 wv[NV][HV], dw[NV][HV], db[NV][HV];
+    load_columns<NV, HV>(w, d, nthr, idx, 1.f, wv);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < HV; ++e) dw[v][e] = db[v][e] = both(0.f);
+    float mu_n[R], rs_n[R];              // the statistics of the group's rows, loaded one batch ahead
+    auto fetch = [&](int64_t i) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = i * B + first + r;
+            mu_n[r] = row < Tn ? __ldg(mean + row) : 0.f;
+            rs_n[r] = row < Tn ? __ldg(rstd + row) : 0.f;
+        }
+    };
+    fetch(blockIdx.x);
+    for (int64_t i = blockIdx.x; i < batches; i += gridDim.x, ring.next()) {
+        float mu[R], rs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mu[r] = mu_n[r];
+            rs[r] = rs_n[r];
+        }
+        fetch(i + gridDim.x);
+        ring.wait(ring.full(), ring.parity);
+        const T* xs = reinterpret_cast<const T*>(smem + (int64_t)ring.s * 2 * B * row_bytes) + (int64_t)first * d;
+        const T* gs = xs + (int64_t)B * d;
+        uint4 xr[R][NV], gr[R][NV];
+        float2 sg[R], sx[R];                         // sums of g, of g xh
+#pragma unroll
+        for (int r = 0; r < R; ++r) sg[r] = sx[r] = both(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * nthr + idx) * VEC;
+            if (c >= d) continue;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool in = i * B + first + r < Tn;      // else the slot's last contents
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                xr[r][v] = in ? *reinterpret_cast<const uint4*>(xs + (int64_t)r * d + c) : zero;
+                gr[r][v] = in ? *reinterpret_cast<const uint4*>(gs + (int64_t)r * d + c) : zero;
+                float2 xf[HV], gf[HV];
+                pairs_of(xr[r][v], xf);
+                pairs_of(gr[r][v], gf);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) {
+                    const float2 xh = __fmul2_rn(__fadd2_rn(xf[e], both(-mu[r])), both(rs[r]));
+                    const float2 g = __fmul2_rn(gf[e], wv[v][e]);
+                    dw[v][e] = __ffma2_rn(gf[e], xh, dw[v][e]);
+                    db[v][e] = __fadd2_rn(db[v][e], gf[e]);
+                    sg[r] = __fadd2_rn(sg[r], g);
+                    sx[r] = __ffma2_rn(g, xh, sx[r]);
+                }
+            }
+        }
+        float sums[2 * R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            sums[r] = sg[r].x + sg[r].y;
+            sums[R + r] = sx[r].x + sx[r].y;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ring.empty());
+        if (!dx) continue;
+        group_sum<2 * R, G>(sums, buf, phase, nthr);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * nthr + idx) * VEC;
+            if (c >= d) continue;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t row = i * B + first + r;
+                if (row >= Tn) break;
+                // dx = rs g w - (rs q) xh - rs a
+                const float2 a = both(-rs[r] * (sums[r] * inv_d)), q = both(-rs[r] * (sums[R + r] * inv_d) * rs[r]);
+                float2 xf[HV], gf[HV];
+                pairs_of(xr[r][v], xf);
+                pairs_of(gr[r][v], gf);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) {
+                    const float2 t = __ffma2_rn(__fadd2_rn(xf[e], both(-mu[r])), q, a);
+                    gf[e] = __ffma2_rn(__fmul2_rn(gf[e], wv[v][e]), both(rs[r]), t);
+                }
+                st_v4(dx + row * d + c, vector_of(gf));
+            }
+        }
+    }
+    if (!part) return;
+    float* pw = part + (int64_t)blockIdx.x * 2 * d;
+    if constexpr (G != 0) {
+        // the block's groups add their sums in turn, over the ring (every row in it has been read)
+        float* cols = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+        for (int k = 0; k < GROUPS; ++k) {
+            if (k % (32 / (G ? G : 32)) == 0) asm volatile("bar.sync 1, %0;" :: "r"(consumers) : "memory");
+            __syncwarp();
+            if (group == k) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int c = (v * nthr + idx) * VEC;
+                    if (c < d)
+#pragma unroll
+                        for (int e = 0; e < HV; ++e) {
+                            float2* cw = reinterpret_cast<float2*>(cols + c + 2 * e);
+                            float2* cb = reinterpret_cast<float2*>(cols + d + c + 2 * e);
+                            *cw = k ? __fadd2_rn(*cw, dw[v][e]) : dw[v][e];
+                            *cb = k ? __fadd2_rn(*cb, db[v][e]) : db[v][e];
+                        }
+                }
+            }
+        }
+        asm volatile("bar.sync 1, %0;" :: "r"(consumers) : "memory");
+        for (int c = threadIdx.x; c < 2 * d; c += consumers) pw[c] = cols[c];
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * nthr + idx) * VEC;
+            if (c < d)
+#pragma unroll
+                for (int e = 0; e < HV; ++e) {
+                    *reinterpret_cast<float2*>(pw + c + 2 * e) = dw[v][e];
+                    *reinterpret_cast<float2*>(pw + d + c + 2 * e) = db[v][e];
+                }
+        }
+    }
+}
+
+// out[c] = sum over the P blocks of part[p][c], c < 2 d: a block takes 32 columns, its 16 warps a
+// strided share of the rows each, eight loads in flight, added in a fixed order
+__global__ void __launch_bounds__(512)
 ln_cols_kernel(const float* __restrict__ part, int P, int d, float* __restrict__ dw, float* __restrict__ db) {
-    __shared__ float sm[8][33];
+    __shared__ float sm[16][33];
     pdl_launch_next();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane, ld = 2 * (int64_t)d;
     float s = 0.f;
-    if (c < 2 * (int64_t)d)
-        for (int p = warp; p < P; p += 8) s += part[(int64_t)p * 2 * d + c];
+    if (c < ld) {
+        for (int p = warp; p < P; p += 128) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = p + 16 * j < P ? __ldcg(part + (int64_t)(p + 16 * j) * ld + c) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += v[j];
+        }
+    }
     sm[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < 2 * (int64_t)d) {
+    if (warp == 0 && c < ld) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k) s += sm[k][lane];
+        for (int k = 1; k < 16; ++k) s += sm[k][lane];
         if (c < d) {
             if (dw) dw[c] = s;
         } else if (db) {
@@ -426,26 +940,107 @@ cudaError_t bwd(const LnArgs& a, int* blocks) {
     int cap;
     const cudaError_t e = resident(kern, threads, smem, want, &cap);
     if (e != cudaSuccess) return e;
-    if (cap > BWD_BLOCKS) cap = BWD_BLOCKS;
+    if (cap > bwd_blocks(a.d)) cap = bwd_blocks(a.d);
     *blocks = (int)(want < cap ? want : cap);
     return launch_pdl(kern, dim3((unsigned)*blocks), dim3(threads), smem, a.stream, static_cast<const T*>(a.x), a.w,
                       a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part);
 }
 
-// The layout of a row by its length in vectors: a warp up to 4 vectors per lane, a block with 2
-// (then 4) vectors per thread above that, and element-wise access where rows are not 16-byte
-// aligned.  Few rows (at most one block per SM) take one vector per thread: the row's latency counts.
+// Launch shape of a ring kernel: threads, rows per slot, and slots.  The SM's shared memory goes to
+// about 640 threads' worth of blocks.
+struct RingShape {
+    int threads, B, slots;
+    size_t bytes;
+};
+
+template <typename T>
+RingShape ring_shape(int d, int nv, int r, int g, int tensors) {
+    RingShape s{};
+    const int chunks = d / Vec16<T>::VEC, consumers = g ? 32 * WARPS : ((chunks + nv - 1) / nv + 31) / 32 * 32;
+    const int blocks = consumers >= 320 ? 3 : consumers <= 64 ? 10 : 640 / consumers;
+    s.threads = consumers + 32;
+    s.B = g ? WARPS * (32 / g) * r : r;
+    const size_t slot = (size_t)tensors * s.B * d * sizeof(T);
+    s.slots = (int)(204800 / blocks / slot);
+    s.slots = s.slots < 2 ? 2 : s.slots > MAX_SLOTS ? MAX_SLOTS : s.slots;
+    s.bytes = s.slots * slot;
+    return s;
+}
+
+template <typename T, int NV, int R, int G, int TH>
+cudaError_t fwd_ring(const LnArgs& a) {
+    const RingShape r = ring_shape<T>(a.d, NV, R, G, 1);
+    auto kern = ln_fwd_ring_kernel<T, NV, R, G, TH>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)r.bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.T + r.B - 1) / r.B;
+    int cap;
+    e = resident(kern, r.threads, r.bytes, want, &cap);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)(want < cap ? want : cap)), dim3(r.threads), r.bytes, a.stream,
+                      static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd,
+                      r.slots);
+}
+
+template <typename T, int NV, int R, int G, int TH>
+cudaError_t bwd_ring(const LnArgs& a, int* blocks) {
+    const RingShape r = ring_shape<T>(a.d, NV, R, G, 2);
+    auto kern = ln_bwd_ring_kernel<T, NV, R, G, TH>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)r.bytes);
+    if (e != cudaSuccess) return e;
+    // four rows per block at least: a block's column sums cost as much traffic as its first two rows
+    const int64_t batches = (a.T + r.B - 1) / r.B, want = r.B >= 4 ? batches : (batches * r.B + 3) / 4;
+    int cap;
+    e = resident(kern, r.threads, r.bytes, want, &cap);
+    if (e != cudaSuccess) return e;
+    if (cap > bwd_blocks(a.d)) cap = bwd_blocks(a.d);
+    *blocks = (int)(want < cap ? want : cap);
+    return launch_pdl(kern, dim3((unsigned)*blocks), dim3(r.threads), r.bytes, a.stream, static_cast<const T*>(a.x),
+                      a.w, a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part,
+                      r.slots);
+}
+
+template <typename T, int NV>
+cudaError_t fwd_warp(const LnArgs& a) {
+    constexpr int TH = 256;
+    auto kern = ln_fwd_warp_kernel<T, NV>;
+    // the SM's shared memory in equal parts
+    const size_t wb = (size_t)2 * NV * 32 * Vec16<T>::VEC * 4, slot = (size_t)(TH / 32) * a.d * sizeof(T);
+    int slots = (int)((204800 / WARP_BLOCKS<NV> - wb) / slot);
+    slots = slots < 1 ? 1 : slots > WARP_SLOTS ? WARP_SLOTS : slots;
+    const size_t smem = wb + slots * slot;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.T + TH / 32 - 1) / (TH / 32);
+    int cap;
+    e = resident(kern, TH, smem, want, &cap);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)(want < cap ? want : cap)), dim3(TH), smem, a.stream,
+                      static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd, slots);
+}
+
+// The layout of a row by its length in vectors: 8, 16 or 32 lanes with one vector each, 32 with two,
+// a block with two (then four) vectors per thread above that.  At most one row per SM takes a register
+// kernel.
 template <typename T>
 cudaError_t fwd_t(const LnArgs& a, int sms) {
     constexpr int V = Vec16<T>::VEC;
     if (a.d % V == 0 && rows16(a.x) && rows16(a.y)) {
         const int c = a.d / V;
-        if (c <= 32) return fwd<T, V, 1, 4, true>(a);
         if (c <= 1024 && a.T <= sms) return fwd<T, V, 1, 1, false>(a);
-        if (c <= 64) return fwd<T, V, 2, 2, true>(a);
-        if (c <= 128) return fwd<T, V, 4, 1, true>(a);
-        if (c <= 1024) return fwd<T, V, 2, 2, false>(a);
-        if (c <= 2048) return fwd<T, V, 4, 1, false>(a);
+        constexpr int W = 32 * WARPS;
+        if (c <= 8) return fwd_ring<T, 1, 2, 8, W>(a);
+        if (c <= 16) return fwd_ring<T, 1, 2, 16, W>(a);
+        if (c <= 32) return fwd_ring<T, 1, 2, 32, W>(a);
+        if (c <= 64) return fwd_ring<T, 2, 2, 32, W>(a);
+        if (c <= 128) return fwd_warp<T, 4>(a);
+        if (c <= 192) return fwd_warp<T, 6>(a);
+        if (c <= 256) return fwd_warp<T, 8>(a);
+        if (c <= 320) return fwd_warp<T, 10>(a);
+        if (c <= 384) return fwd_warp<T, 12>(a);
+        if (c <= 512) return fwd_warp<T, 16>(a);
+        if (c <= 1024) return fwd_ring<T, 2, 2, 0, 512>(a);
+        if (c <= 2048) return fwd_ring<T, 4, 1, 0, 512>(a);
     } else {
         if (a.d <= 256) return fwd<T, 1, 8, 2, true>(a);
         if (a.d <= 4096) return fwd<T, 1, 8, 2, false>(a);
@@ -459,15 +1054,20 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
 }
 
 template <typename T>
-cudaError_t bwd_t(const LnArgs& a, int* blocks) {
+cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
     constexpr int V = Vec16<T>::VEC;
     if (a.d % V == 0 && rows16(a.x) && rows16(a.dy) && rows16(a.dx)) {
         const int c = a.d / V;
-        if (c <= 32) return bwd<T, V, 1, 2, true>(a, blocks);
-        if (c <= 64) return bwd<T, V, 2, 1, true>(a, blocks);
-        if (c <= 1024) return bwd<T, V, 2, 2, false>(a, blocks);
+        if (c <= 1024 && a.T <= sms) return bwd<T, V, 1, 1, false>(a, blocks);
+        constexpr int W = 32 * WARPS;
+        if (c <= 8) return bwd_ring<T, 1, 2, 8, W>(a, blocks);
+        if (c <= 16) return bwd_ring<T, 1, 2, 16, W>(a, blocks);
+        if (c <= 32) return bwd_ring<T, 1, 2, 32, W>(a, blocks);
+        if (c <= 64) return bwd_ring<T, 2, 1, 32, W>(a, blocks);
+        if (c <= 512) return bwd_ring<T, 2, 2, 0, 256>(a, blocks);
+        if (c <= 1024) return bwd_ring<T, 2, 1, 0, 512>(a, blocks);
         if constexpr (V == 4) {
-            if (c <= 2048) return bwd<T, V, 4, 1, false>(a, blocks);
+            if (c <= 2048) return bwd_ring<T, 4, 1, 0, 512>(a, blocks);
         }
     } else {
         if (a.d <= 256) return bwd<T, 1, 8, 1, true>(a, blocks);
@@ -477,7 +1077,7 @@ cudaError_t bwd_t(const LnArgs& a, int* blocks) {
     int cap;
     cudaError_t e = resident(ln_bwd_long_kernel<T>, 1024, 0, a.T, &cap);
     if (e != cudaSuccess) return e;
-    if (cap > BWD_BLOCKS) cap = BWD_BLOCKS;
+    if (cap > bwd_blocks(a.d)) cap = bwd_blocks(a.d);
     *blocks = (int)(a.T < cap ? a.T : cap);
     return launch_pdl(ln_bwd_long_kernel<T>, dim3((unsigned)*blocks), dim3(1024), 0, a.stream,
                       static_cast<const T*>(a.x), a.w, a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d,
@@ -487,7 +1087,7 @@ cudaError_t bwd_t(const LnArgs& a, int* blocks) {
 }  // namespace
 
 int64_t layer_norm_part_floats(int64_t T, int d) {
-    const int64_t p = T < BWD_BLOCKS ? T : BWD_BLOCKS;
+    const int64_t p = T < bwd_blocks(d) ? T : bwd_blocks(d);
     return p * 2 * d;
 }
 
@@ -499,11 +1099,24 @@ cudaError_t launch_layer_norm(const LnArgs& a) {
 }
 
 cudaError_t launch_layer_norm_backward(const LnArgs& a) {
+    DeviceInfo di;
+    cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
     int blocks = 0;
-    cudaError_t e = a.dt == BF16 ? bwd_t<__nv_bfloat16>(a, &blocks) : bwd_t<float>(a, &blocks);
+    e = a.dt == BF16 ? bwd_t<__nv_bfloat16>(a, di.sm_count, &blocks) : bwd_t<float>(a, di.sm_count, &blocks);
     if (e != cudaSuccess || !a.part) return e;
     const unsigned grid = (unsigned)((2 * (int64_t)a.d + 31) / 32);
-    return launch_pdl(ln_cols_kernel, dim3(grid), dim3(256), 0, a.stream, a.part, blocks, a.d, a.dw, a.db);
+    return launch_pdl(ln_cols_kernel, dim3(grid), dim3(512), 0, a.stream, a.part, blocks, a.d, a.dw, a.db);
+}
+
+cudaError_t layer_norm_status(unsigned* out, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_layer_norm_status, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    if (clear && *out) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_layer_norm_status, &zero, sizeof(unsigned));
+    }
+    return e;
 }
 
 }  // namespace mhc

@@ -354,13 +354,14 @@ mhc_status mhc_debug_backward_stop_after(int32_t stages, uint32_t wait_limit_us)
 
 mhc_status mhc_device_status(uint32_t* code) {
     if (!code) return MHC_ERR_NULL;
-    unsigned v = 0, w = 0, b = 0, l = 0;
+    unsigned v = 0, w = 0, b = 0, l = 0, ln = 0;
     cudaError_t e = pre_tc_status(&v, true);
     if (e == cudaSuccess) e = pre_wide_status(&w, true);
     if (e == cudaSuccess) e = bwd_tc_status(&b, true);
     if (e == cudaSuccess) e = linear_tc_status(&l, true);
+    if (e == cudaSuccess) e = layer_norm_status(&ln, true);
     if (e != cudaSuccess) return cuda_fail(e, "mhc_device_status");
-    *code = v | (w << 16) | (b << 24) | (l << 29);
+    *code = v | (w << 16) | (b << 24) | ((l | ln) << 29);
     return MHC_OK;
 }
 
