@@ -219,11 +219,20 @@ struct GemmArgs {
     DType dt;
     cudaStream_t stream;
 };
-cudaError_t launch_gemm_generic(const GemmArgs& a);
+// Where only_if is given, the kernel does nothing unless one of its only_if_n words is set.
+cudaError_t launch_gemm_generic(const GemmArgs& a, const int* only_if = nullptr, int only_if_n = 0);
 // The same on the tensor cores (linear_tc.cu), for products gemm_tc_ok accepts: bf16 operands whose
 // rows are 16-byte aligned.
 bool gemm_tc_ok(const GemmArgs& a);
 cudaError_t launch_gemm_tc(const GemmArgs& a);
+// An fp32 product on the tensor cores from its operands' bf16 parts (split_rows in linear.cu): three
+// planes of rows of lda (ldb) elements, a_plane (b_plane) elements apart, for the same layouts.
+struct F32Planes {
+    const void* A;
+    const void* B;
+    int64_t lda, ldb, a_plane, b_plane;
+};
+cudaError_t launch_gemm_f32(const GemmArgs& a, const F32Planes& f);
 cudaError_t linear_tc_status(unsigned* out, bool clear);
 
 // Amax Gain Magnitude of composite residual maps (diagnostics.cu).

@@ -189,29 +189,92 @@ int64_t padded(int64_t cols) { return (cols + 7) / 8 * 8; }
 
 cudaError_t product(const GemmArgs& g) { return gemm_tc_ok(g) ? launch_gemm_tc(g) : launch_gemm_generic(g); }
 
+// The bf16 parts h + m + l of fp32 rows, in three planes of rows on 16-byte boundaries.  A value that
+// is not finite, or whose h would not be, has no such parts: its block sets its word of `odd`, and the
+// CUDA-core kernel forms the product instead.
+struct SplitJob {
+    const float* src;
+    __nv_bfloat16* dst;
+    int* odd;                          // SPLIT_BLOCKS words
+    int64_t rows, ld;                  // ld: elements per row of a plane, a multiple of 8
+    int cols;
+};
+constexpr int SPLIT_BLOCKS = 4 * 148;
+
+__global__ void __launch_bounds__(256) split_rows_kernel(const __grid_constant__ SplitJob a, const __grid_constant__ SplitJob b) {
+    const SplitJob& j = blockIdx.y ? b : a;
+    pdl_launch_next();
+    pdl_wait();
+    const int64_t per = j.ld / 8, total = j.rows * per, plane = j.rows * j.ld;
+    const bool vec = j.cols % 4 == 0 && (uintptr_t)j.src % 16 == 0;
+    int odd = 0;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per;
+        const int c = (int)(i - row * per) * 8;
+        const float* s = j.src + row * j.cols + c;
+        float f[8];
+        if (vec && c + 8 <= j.cols) {
+            Vec16<float>::unpack(ld_stream_v4(s), f);
+            Vec16<float>::unpack(ld_stream_v4(s + 4), f + 4);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = c + e < j.cols ? __ldg(s + e) : 0.f;
+        }
+        float h[8], m[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            h[e] = __bfloat162float(__float2bfloat16_rn(f[e]));
+            odd |= !(fabsf(h[e]) <= 3.4028234e38f);
+            f[e] -= h[e];                              // exact, as is the next difference
+            m[e] = __bfloat162float(__float2bfloat16_rn(f[e]));
+            f[e] -= m[e];
+        }
+        __nv_bfloat16* d = j.dst + row * j.ld + c;
+        st_v4(d, Vec16<__nv_bfloat16>::pack(h));
+        st_v4(d + plane, Vec16<__nv_bfloat16>::pack(m));
+        st_v4(d + 2 * plane, Vec16<__nv_bfloat16>::pack(f));
+    }
+    odd = __syncthreads_or(odd);
+    if (threadIdx.x == 0) j.odd[blockIdx.x] = odd;
+}
+
+// every block writes its word, so all SPLIT_BLOCKS of them are set afterwards
+cudaError_t split_rows(const SplitJob& a, const SplitJob& b, cudaStream_t s) {
+    return launch_pdl(split_rows_kernel, dim3(SPLIT_BLOCKS, b.rows ? 2 : 1), dim3(256), 0, s, a, b);
+}
+
+// fp32 products that go to the tensor cores: those whose time on CUDA cores exceeds what the parts
+// cost to make
+bool parts_pay(int64_t T, int K, int N) {
+    return T > 64 && T < ((int64_t)1 << 31) - 1024 && (double)T * K * N >= 1e9;
+}
+
 // Regions of the workspaces, in bytes.  bf16 rows of K elements that are not a multiple of 16 bytes
-// are copied to padded ones (x and W).
+// are copied to padded ones (x and W); fp32 operands of the tensor cores are held in parts.
 struct Regions {
-    size_t x, W, dz, part, total;
-    int64_t ldk, ldn;                  // elements per row of the padded x and W, and of dz
-    bool pad;
+    size_t x, W, dz, part, odd, dzp, total;
+    int64_t ldk, ldn;                  // elements per row of the copies of x and W, and of dz
+    bool pad, parts;
 };
 
 Regions regions(int64_t T, int K, int N, DType dt, bool backward) {
     Regions L{};
     const size_t es = dt == BF16 ? 2 : 4;
     L.pad = dt == BF16 && K % 8 != 0;
-    L.ldk = L.pad ? padded(K) : K;
-    L.ldn = dt == BF16 ? padded(N) : N;
+    L.parts = dt == F32 && parts_pay(T, K, N);
+    L.ldk = L.pad || L.parts ? padded(K) : K;
+    L.ldn = dt == BF16 || L.parts ? padded(N) : N;
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t at = off; off += round256(bytes); return at; };
-    if (L.pad) {
-        L.x = take((size_t)T * L.ldk * es);
-        L.W = take((size_t)N * L.ldk * es);
+    if (L.pad || L.parts) {
+        L.x = take((size_t)T * L.ldk * (L.parts ? 6 : 2));
+        L.W = take((size_t)N * L.ldk * (L.parts ? 6 : 2));
     }
+    if (L.parts) L.odd = take((size_t)3 * SPLIT_BLOCKS * 4);
     if (backward) {
-        L.dz = take((size_t)T * L.ldn * es);
+        L.dz = take((size_t)T * (dt == BF16 ? L.ldn : N) * es);
         L.part = take((size_t)dz_runs(T, N) * N * 4);
+        if (L.parts) L.dzp = take((size_t)T * L.ldn * 6);
     }
     L.total = off;
     return L;
@@ -228,17 +291,29 @@ cudaError_t launch_linear(const LinearArgs& a) {
     unsigned char* ws = static_cast<unsigned char*>(a.workspace);
     GemmArgs g{};
     g.A = a.x; g.B = a.W;
-    g.lda = g.ldb = L.ldk;
-    if (L.pad) {
-        const PadJob x{static_cast<const __nv_bfloat16*>(a.x), reinterpret_cast<__nv_bfloat16*>(ws + L.x), a.T, L.ldk, a.K};
-        const PadJob w{static_cast<const __nv_bfloat16*>(a.W), reinterpret_cast<__nv_bfloat16*>(ws + L.W), a.N, L.ldk, a.K};
-        const cudaError_t e = pad_rows(x, w, a.stream);
-        if (e != cudaSuccess) return e;
-        g.A = x.dst; g.B = w.dst;
-    }
+    g.lda = g.ldb = a.K;
     g.M = a.T; g.N = a.N; g.K = a.K;
     g.bias = a.bias; g.residual = a.residual; g.act = a.act; g.D = a.y; g.z = a.z;
     g.dt = a.dt; g.stream = a.stream;
+    __nv_bfloat16* xc = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
+    __nv_bfloat16* wc = reinterpret_cast<__nv_bfloat16*>(ws + L.W);
+    if (L.parts) {
+        int* odd = reinterpret_cast<int*>(ws + L.odd);
+        const SplitJob x{static_cast<const float*>(a.x), xc, odd, a.T, L.ldk, a.K};
+        const SplitJob w{static_cast<const float*>(a.W), wc, odd + SPLIT_BLOCKS, a.N, L.ldk, a.K};
+        cudaError_t e = split_rows(x, w, a.stream);
+        if (e == cudaSuccess)
+            e = launch_gemm_f32(g, F32Planes{xc, wc, L.ldk, L.ldk, a.T * L.ldk, a.N * L.ldk});
+        return e == cudaSuccess ? launch_gemm_generic(g, odd, 2 * SPLIT_BLOCKS) : e;
+    }
+    if (L.pad) {
+        const PadJob x{static_cast<const __nv_bfloat16*>(a.x), xc, a.T, L.ldk, a.K};
+        const PadJob w{static_cast<const __nv_bfloat16*>(a.W), wc, a.N, L.ldk, a.K};
+        const cudaError_t e = pad_rows(x, w, a.stream);
+        if (e != cudaSuccess) return e;
+        g.A = xc; g.B = wc;
+        g.lda = g.ldb = L.ldk;
+    }
     return product(g);
 }
 
@@ -249,39 +324,53 @@ cudaError_t launch_linear_backward(const LinearArgs& a) {
     // dz is dy itself without an activation, unless the tensor cores need its rows on 16-byte boundaries
     const bool copy = a.act != ACT_NONE || (a.dt == BF16 && (a.N % 8 != 0 || (uintptr_t)a.dy % 16 != 0));
     void* dz = copy && products ? ws + L.dz : nullptr;
+    const int64_t ldz = dz && a.dt == BF16 ? L.ldn : a.N;
     cudaError_t e = cudaSuccess;
     if (dz || a.dbias) {
         float* part = reinterpret_cast<float*>(ws + L.part);
-        e = a.dt == BF16 ? launch_dz<__nv_bfloat16>(a, dz, L.ldn, part) : launch_dz<float>(a, dz, L.ldn, part);
+        e = a.dt == BF16 ? launch_dz<__nv_bfloat16>(a, dz, ldz, part) : launch_dz<float>(a, dz, ldz, part);
     }
-    const void* x = a.x;
-    const void* W = a.W;
-    if (e == cudaSuccess && L.pad && products) {
-        const PadJob none{};
-        const PadJob jx{static_cast<const __nv_bfloat16*>(a.x), reinterpret_cast<__nv_bfloat16*>(ws + L.x), a.T, L.ldk, a.K};
-        const PadJob jw{static_cast<const __nv_bfloat16*>(a.W), reinterpret_cast<__nv_bfloat16*>(ws + L.W), a.N, L.ldk, a.K};
-        e = pad_rows(a.dx ? jw : jx, a.dx && a.dW ? jx : none, a.stream);
-        x = jx.dst;
-        W = jw.dst;
+    if (e != cudaSuccess || !products) return e;
+    __nv_bfloat16* xc = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
+    __nv_bfloat16* wc = reinterpret_cast<__nv_bfloat16*>(ws + L.W);
+    __nv_bfloat16* zc = reinterpret_cast<__nv_bfloat16*>(ws + L.dzp);
+    int* odd = reinterpret_cast<int*>(ws + L.odd);       // of W, dz, x
+    if (L.parts) {
+        const SplitJob jw{static_cast<const float*>(a.W), wc, odd, a.N, L.ldk, a.K};
+        const SplitJob jz{static_cast<const float*>(dz ? dz : a.dy), zc, odd + SPLIT_BLOCKS, a.T, L.ldn, a.N};
+        const SplitJob jx{static_cast<const float*>(a.x), xc, odd + 2 * SPLIT_BLOCKS, a.T, L.ldk, a.K};
+        e = split_rows(jz, a.dx ? jw : jx, a.stream);
+        if (e == cudaSuccess && a.dx && a.dW) e = split_rows(jx, SplitJob{}, a.stream);
+    } else if (L.pad) {
+        const PadJob jw{static_cast<const __nv_bfloat16*>(a.W), wc, a.N, L.ldk, a.K};
+        const PadJob jx{static_cast<const __nv_bfloat16*>(a.x), xc, a.T, L.ldk, a.K};
+        e = pad_rows(a.dx ? jw : jx, a.dx && a.dW ? jx : PadJob{}, a.stream);
     }
+    if (e != cudaSuccess) return e;
     GemmArgs g{};
     g.A = dz ? dz : a.dy;
-    g.lda = dz ? L.ldn : a.N;
+    g.lda = ldz;
     g.dt = a.dt; g.stream = a.stream; g.act = ACT_NONE;
     g.b_mn = true;
-    g.ldb = L.ldk;
-    if (e == cudaSuccess && a.dx) {          // dx[t][k] = sum_n dz[t][n] W[n][k]
-        g.B = W;
+    g.ldb = L.pad ? L.ldk : a.K;
+    // one of the two products, with the words of its operands
+    auto run = [&](const void* B, const __nv_bfloat16* parts, int64_t b_rows, const int* words) {
+        g.B = L.pad ? parts : B;
+        if (!L.parts) return product(g);
+        cudaError_t r = launch_gemm_f32(g, F32Planes{zc, parts, L.ldn, L.ldk, a.T * L.ldn, b_rows * L.ldk});
+        if (r == cudaSuccess) r = launch_gemm_generic(g, words, 2 * SPLIT_BLOCKS);
+        return r;
+    };
+    if (a.dx) {                              // dx[t][k] = sum_n dz[t][n] W[n][k]
         g.M = a.T; g.N = a.K; g.K = a.N;
         g.D = a.dx;
-        e = product(g);
+        e = run(a.W, wc, a.N, odd);
     }
     if (e == cudaSuccess && a.dW) {          // dW[n][k] = sum_t dz[t][n] x[t][k]
         g.a_mn = true;
-        g.B = x;
         g.M = a.N; g.N = a.K; g.K = a.T;
         g.D = a.dW;
-        e = product(g);
+        e = run(a.x, xc, a.T, odd + SPLIT_BLOCKS);
     }
     return e;
 }

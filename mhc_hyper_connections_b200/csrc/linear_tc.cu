@@ -144,6 +144,12 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
                  " [%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(cluster_bar) : "memory");
 }
+__device__ __forceinline__ void tma_load_pair_3d(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int c0,
+                                                 int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar) : "memory");
+}
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
 }
@@ -177,14 +183,85 @@ struct Maps {
     CUtensorMap a, b;
 };
 
+template <typename T>
 struct Epilogue {
     const float* bias;
-    const bf16* residual;
-    bf16* D;
-    bf16* z;
+    const T* residual;
+    T* D;
+    T* z;
     int act;
     int vec;                             // rows of D, z and residual are 16-byte aligned
 };
+
+// The outputs of a warp's 32 rows x 128 bytes of columns at (r0, c0) from their sums, a row per lane:
+// v = act(v + bias) + residual, and z.  Between registers and memory (128 bytes of a row per eight
+// lanes) the block goes through the warp's 4 KB of shared memory, swizzled by 16-byte chunks.
+template <typename T>
+__device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[ROW / sizeof(T)], unsigned char* out,
+                                             int64_t r0, int64_t c0, int64_t M, int64_t N, int lane) {
+    constexpr int CW = ROW / sizeof(T), VEC = Vec16<T>::VEC;
+    auto at = [&](int r, int j) { return out + r * ROW + ((j ^ (r & 7)) << 4); };
+    auto put = [&](T* dst) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at(lane, j)) = Vec16<T>::pack(v + VEC * j);
+        __syncwarp();
+        if (ep.vec) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const int r = 4 * p + (lane >> 3), j = lane & 7;
+                if (r0 + r < M && c0 + VEC * j < N)
+                    st_v4(dst + (r0 + r) * N + c0 + VEC * j, *reinterpret_cast<const uint4*>(at(r, j)));
+            }
+        } else {
+#pragma unroll 2
+            for (int r = 0; r < 32 && r0 + r < M; ++r)
+#pragma unroll
+                for (int u = 0; u < CW / 32; ++u) {
+                    const int c = lane + 32 * u;
+                    if (c0 + c < N) dst[(r0 + r) * N + c0 + c] = reinterpret_cast<const T*>(at(r, c / VEC))[c % VEC];
+                }
+        }
+        __syncwarp();
+    };
+    if (ep.bias) {
+#pragma unroll
+        for (int j = 0; j < CW; ++j) v[j] += c0 + j < N ? __ldg(ep.bias + c0 + j) : 0.f;
+    }
+    if (ep.z) put(ep.z);
+    if (ep.residual) {
+        if (ep.vec) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const int r = 4 * p + (lane >> 3), j = lane & 7;
+                if (r0 + r < M && c0 + VEC * j < N)
+                    *reinterpret_cast<uint4*>(at(r, j)) = ld_stream_v4(ep.residual + (r0 + r) * N + c0 + VEC * j);
+            }
+        } else {
+#pragma unroll 2
+            for (int r = 0; r < 32 && r0 + r < M; ++r)
+#pragma unroll
+                for (int u = 0; u < CW / 32; ++u) {
+                    const int c = lane + 32 * u;
+                    if (c0 + c < N) reinterpret_cast<T*>(at(r, c / VEC))[c % VEC] = ep.residual[(r0 + r) * N + c0 + c];
+                }
+        }
+        __syncwarp();
+    }
+    with_act(ep.act, [&](auto kind) {
+#pragma unroll
+        for (int j = 0; j < CW; ++j) v[j] = act_value<kind(), sizeof(T) == 2>(v[j]);
+    });
+    if (ep.residual) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float f[VEC];
+            Vec16<T>::unpack(*reinterpret_cast<uint4*>(at(lane, j)), f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v[VEC * j + e] += f[e];
+        }
+    }
+    put(ep.D);                           // a lane overwrites its own row of the residual
+}
 
 // ------------------------------------------------------------------------- the pair kernel
 
@@ -218,7 +295,7 @@ __device__ __forceinline__ void tile_at(int64_t i, int mt, int nt, int& m, int& 
 
 template <int BN, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue ep, int64_t M, int64_t N, int kblocks, int mt,
+gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<bf16> ep, int64_t M, int64_t N, int kblocks, int mt,
                  int nt, unsigned long long wait_ns) {
     using C = PairCfg<BN>;
     constexpr int NS = C::NS, KS = C::KS;
@@ -364,76 +441,201 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
                 float v[64];
                 tmem_ld32(tq + buf * BN + h * (BN / 2) + cc, reinterpret_cast<float(&)[32]>(v[0]));
                 tmem_ld32(tq + buf * BN + h * (BN / 2) + cc + 32, reinterpret_cast<float(&)[32]>(v[32]));
-                // this warp's 32 x 64 block between registers (a row per lane) and memory (128 bytes
-                // of a row per eight lanes), through shared memory swizzled by 16-byte chunks
-                auto at = [&](int r, int j) { return out + r * ROW + ((j ^ (r & 7)) << 4); };
-                auto put = [&](bf16* dst) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at(lane, j)) = Vec16<bf16>::pack(v + 8 * j);
-                    __syncwarp();
-                    if (ep.vec) {
-#pragma unroll
-                        for (int p = 0; p < 8; ++p) {
-                            const int r = 4 * p + (lane >> 3), j = lane & 7;
-                            if (r0 + r < M && c0 + 8 * j < N)
-                                st_v4(dst + (r0 + r) * N + c0 + 8 * j, *reinterpret_cast<const uint4*>(at(r, j)));
-                        }
-                    } else {
-#pragma unroll 2
-                        for (int r = 0; r < 32 && r0 + r < M; ++r)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int c = lane + 32 * u;
-                                if (c0 + c < N)
-                                    dst[(r0 + r) * N + c0 + c] = reinterpret_cast<const bf16*>(at(r, c >> 3))[c & 7];
-                            }
-                    }
-                    __syncwarp();
-                };
-                if (ep.bias) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] += c0 + j < N ? __ldg(ep.bias + c0 + j) : 0.f;
-                }
-                if (ep.z) put(ep.z);
-                if (ep.residual) {
-                    if (ep.vec) {
-#pragma unroll
-                        for (int p = 0; p < 8; ++p) {
-                            const int r = 4 * p + (lane >> 3), j = lane & 7;
-                            if (r0 + r < M && c0 + 8 * j < N)
-                                *reinterpret_cast<uint4*>(at(r, j)) =
-                                    ld_stream_v4(ep.residual + (r0 + r) * N + c0 + 8 * j);
-                        }
-                    } else {
-#pragma unroll 2
-                        for (int r = 0; r < 32 && r0 + r < M; ++r)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int c = lane + 32 * u;
-                                if (c0 + c < N)
-                                    reinterpret_cast<bf16*>(at(r, c >> 3))[c & 7] = ep.residual[(r0 + r) * N + c0 + c];
-                            }
-                    }
-                    __syncwarp();
-                }
-                with_act(ep.act, [&](auto kind) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = act_value<kind(), true>(v[j]);
-                });
-                if (ep.residual) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float f[8];
-                        Vec16<bf16>::unpack(*reinterpret_cast<uint4*>(at(lane, j)), f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[8 * j + e] += f[e];
-                    }
-                }
-                put(ep.D);               // a lane overwrites its own row of the residual
+                finish_block<bf16>(ep, v, out, r0, c0, M, N, lane);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(acce_first[buf]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tm, C::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------------- fp32 operands
+//
+// An fp32 value is the sum of three bf16 ones, h + m + l, 8 significant bits each.  Of the nine products
+// of two such sums the six above 2^-24 of the whole are formed; the products of a chunk of K add up in
+// TMEM, the chunks in registers.  The tensor core's additions drop the bits below its accumulator
+// instead of rounding, an error of one sign that grows with the number of additions.  So a chunk is
+// short (CHUNK blocks of 64), and the five small products have an accumulator of their own, where the
+// dropped bits are 2^-8 of those of h h (one accumulator for all six: a relative error of 1.5e-6 at
+// any K; see linear.cu for when this kernel runs).
+
+struct F32Cfg {
+    static constexpr int BN = 128;
+    static constexpr int A_PLANE = 128 * ROW, B_PLANE = BN / 2 * ROW;      // one of the three parts
+    static constexpr int STAGE = 3 * (A_PLANE + B_PLANE);                  // 64 of K
+    static constexpr int NS = 2;
+    static constexpr int OUT = EPI * 32 * ROW;
+    static constexpr int SMEM = NS * STAGE + OUT + 1024;
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int CHUNK = 4;
+    static_assert(SMEM <= 232448 - 512, "shared memory");
+};
+
+// The maps cover the planes as a third dimension and bring the three parts of a box together: rows
+// along K as [part][row], others as [64 rows][part][64 of K].
+template <bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<float> ep, int64_t M, int64_t N,
+                int kblocks, int mt, int nt, unsigned long long wait_ns) {
+    using C = F32Cfg;
+    constexpr int NS = C::NS, BN = C::BN;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ __align__(8) uint64_t bars[2 * NS + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    auto full = [&](int s) { return smem_u32(&bars[s]); };
+    auto empty = [&](int s) { return smem_u32(&bars[NS + s]); };
+    auto accf = [&](int b) { return smem_u32(&bars[2 * NS + b]); };
+    auto acce = [&](int b) { return smem_u32(&bars[2 * NS + 2 + b]); };
+    const uint32_t drained = smem_u32(&bars[2 * NS + 4]);
+    const Waiter wait{&abort_flag, wait_ns};
+    const Waiter drain{&abort_flag, wait_ns > kDrainNs ? wait_ns : kDrainNs};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank(), base = smem_u32(sm);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf(b), 1);
+            mbar_init(acce(b), 2 * EPI);
+        }
+        mbar_init(drained, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_slot), C::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    pdl_launch_next();                   // as in the pair kernel
+    pdl_wait();
+    const uint32_t tm = tmem_slot;
+    const int64_t tiles = (int64_t)mt * nt;
+    const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+    if (warp == 0) {
+        Ring<NS> ring;
+        bool ok = true;
+        for (int64_t i = first; ok && i < tiles; i += stride) {
+            int m, n;
+            tile_at(i, mt, nt, m, n);
+            const int m0 = m * 256 + (int)rank * 128, n0 = n * BN + (int)rank * (BN / 2);
+            for (int kb = 0; kb < kblocks; ++kb, ring.next()) {
+                const int s = ring.s;
+                if (!(ok = wait.warp(empty(s), ring.parity ^ 1u, E_STAGE))) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_tx(full(s), 2 * C::STAGE);
+                    const uint32_t bar = mapa(full(s), 0);
+                    const uint32_t a = base + s * C::STAGE, b = a + 3 * C::A_PLANE;
+                    const int k = kb * BK;
+                    if constexpr (A_MN) {
+                        tma_load_pair_3d(a, &maps.a, bar, m0, k, 0);
+                        tma_load_pair_3d(a + 3 * BLK, &maps.a, bar, m0 + 64, k, 0);
+                    } else {
+                        tma_load_pair_3d(a, &maps.a, bar, k, m0, 0);
+                    }
+                    if constexpr (B_MN) {
+                        tma_load_pair_3d(b, &maps.b, bar, n0, k, 0);
+                    } else {
+                        tma_load_pair_3d(b, &maps.b, bar, k, n0, 0);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        for (int j = 0; ok && j < NS; ++j, ring.next()) ok = wait.warp(empty(ring.s), ring.parity ^ 1u, E_STAGE);
+        if (!ok) pause_ns(kLandNs);
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            constexpr uint32_t ID = idesc(256, BN, A_MN, B_MN);
+            // parts of A and B in each product, smallest products first
+            constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
+            constexpr uint32_t AP = (A_MN ? BLK : C::A_PLANE) >> 4, BP = (B_MN ? BLK : C::B_PLANE) >> 4;
+            const uint64_t da0 = A_MN ? sw128_desc_mn(base, 3 * BLK, 1024) : sw128_desc(base);
+            const uint64_t db0 = base_desc<B_MN>(base + 3 * C::A_PLANE);
+            Ring<NS> ring;
+            int tc = 0;
+            bool ok = true;
+            for (int64_t i = first; ok && i < tiles; i += stride) {
+                for (int kb = 0; ok && kb < kblocks; ++tc) {
+                    const int buf = tc & 1;
+                    if (!(ok = wait.warp(acce(buf), ((uint32_t)(tc >> 1) & 1u) ^ 1u, E_ACC))) break;
+                    tc_fence_after();
+                    const int end = kb + C::CHUNK < kblocks ? kb + C::CHUNK : kblocks;
+                    for (bool fresh = true; kb < end; ++kb, fresh = false, ring.next()) {
+                        const int s = ring.s;
+                        if (!(ok = wait.warp(full(s), ring.parity, E_STAGE))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t off = (uint32_t)(s * (C::STAGE >> 4));
+#pragma unroll
+                            for (int p = 0; p < 6; ++p)
+#pragma unroll
+                                for (int k = 0; k < BK / 16; ++k)
+                                    mma_pair(tm + buf * 2 * BN + (p < 5 ? BN : 0), da0 + off + PA[p] * AP + k * K16<A_MN>,
+                                             db0 + off + PB[p] * BP + k * K16<B_MN>, ID,
+                                             (!fresh || (p > 0 && p < 5) || k > 0) ? 1u : 0u);
+                            mma_commit_pair(empty(s));
+                            if (kb == end - 1) mma_commit_pair(accf(buf));
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (!ok) {
+                if (elect_one())
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                                 :: "r"(drained) : "memory");
+                drain.warp(drained, 0u, E_DRAIN, false);
+            }
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, h = (warp - 2) >> 2;
+        const uint32_t tq = tm + ((uint32_t)(32 * q) << 16) + h * (BN / 2);
+        unsigned char* out = sm + NS * C::STAGE + (warp - 2) * 32 * ROW;
+        const uint32_t acce_first[2] = {mapa(acce(0), 0), mapa(acce(1), 0)};
+        int tc = 0;
+        bool ok = true;
+        for (int64_t i = first; ok && i < tiles; i += stride) {
+            int m, n;
+            tile_at(i, mt, nt, m, n);
+            const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q, c0 = (int64_t)n * BN + h * (BN / 2);
+            float sum[2][32] = {};
+            for (int kb = 0; kb < kblocks; kb += C::CHUNK, ++tc) {
+                const int buf = tc & 1;
+                if (!(ok = wait.warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float v[32], w[32];
+                    tmem_ld32(tq + buf * 2 * BN + 32 * u, v);
+                    tmem_ld32(tq + buf * 2 * BN + BN + 32 * u, w);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[u][j] += v[j] + w[j];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(buf ? acce_first[1] : acce_first[0]);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (c0 + 32 * u < N && r0 < M) finish_block<float>(ep, sum[u], out, r0, c0 + 32 * u, M, N, lane);
         }
     }
     tc_fence_before();
@@ -465,7 +667,7 @@ struct SplitCfg {
 // one.  bias belongs to r.
 template <int BN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(THREADS, SplitCfg<BN>::PER_SM)
-gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue ep, int64_t Mr, int64_t Nc, int kblocks, int mt,
+gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<bf16> ep, int64_t Mr, int64_t Nc, int kblocks, int mt,
                   int S, unsigned long long wait_ns) {
     using C = SplitCfg<BN>;
     constexpr int NS = C::NS, KS = C::KS;
@@ -692,6 +894,20 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t K, int64_t 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The three planes of an fp32 operand, `plane` elements apart: boxes of 64 x (box_rows or 64) x 3
+bool make_map_planes(CUtensorMap* map, const void* p, int64_t rows, int64_t K, int64_t ld, int64_t plane, bool mn,
+                     int box_rows) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)(mn ? rows : K), (cuuint64_t)(mn ? K : rows), 3};
+    const cuuint64_t str[2] = {(cuuint64_t)ld * 2, (cuuint64_t)plane * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(mn ? 64 : box_rows), 3};
+    const cuuint32_t e1[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, str, box, e1,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 std::atomic<unsigned long long> g_wait_ns{kWaitNs};
 
 template <typename K>
@@ -699,14 +915,16 @@ cudaError_t allow_smem(K kern, int bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-Epilogue epilogue_of(const GemmArgs& g) {
-    Epilogue ep;
+template <typename T>
+Epilogue<T> epilogue_of(const GemmArgs& g) {
+    Epilogue<T> ep;
     ep.bias = g.bias;
-    ep.residual = static_cast<const bf16*>(g.residual);
-    ep.D = static_cast<bf16*>(g.D);
-    ep.z = static_cast<bf16*>(g.z);
+    ep.residual = static_cast<const T*>(g.residual);
+    ep.D = static_cast<T*>(g.D);
+    ep.z = static_cast<T*>(g.z);
     ep.act = g.act;
-    ep.vec = g.N % 8 == 0 && (uintptr_t)g.D % 16 == 0 && (uintptr_t)g.z % 16 == 0 && (uintptr_t)g.residual % 16 == 0;
+    ep.vec = g.N % Vec16<T>::VEC == 0 && (uintptr_t)g.D % 16 == 0 && (uintptr_t)g.z % 16 == 0 &&
+             (uintptr_t)g.residual % 16 == 0;
     return ep;
 }
 
@@ -722,7 +940,7 @@ cudaError_t pair_launch(const GemmArgs& g, int sms) {
     const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + BN - 1) / BN);
     const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_pdl(kern, dim3(grid), dim3(THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of(g), g.M, g.N,
+    return launch_pdl(kern, dim3(grid), dim3(THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<bf16>(g), g.M, g.N,
                       (int)((g.K + BK - 1) / BK), mt, nt, g_wait_ns.load());
 }
 
@@ -730,6 +948,23 @@ template <int BN>
 cudaError_t pair_layout(const GemmArgs& g, int sms) {
     if (g.a_mn) return g.b_mn ? pair_launch<BN, true, true>(g, sms) : cudaErrorInvalidValue;
     return g.b_mn ? pair_launch<BN, false, true>(g, sms) : pair_launch<BN, false, false>(g, sms);
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t f32_launch(const GemmArgs& g, const F32Planes& f, int sms) {
+    using C = F32Cfg;
+    auto kern = gemm_f32_kernel<A_MN, B_MN>;
+    cudaError_t e = allow_smem(kern, C::SMEM);
+    if (e != cudaSuccess) return e;
+    Maps maps;
+    if (!make_map_planes(&maps.a, f.A, g.M, g.K, f.lda, f.a_plane, A_MN, 128) ||
+        !make_map_planes(&maps.b, f.B, g.N, g.K, f.ldb, f.b_plane, B_MN, C::BN / 2))
+        return cudaErrorInvalidValue;
+    const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + C::BN - 1) / C::BN);
+    const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
+    const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
+    return launch_pdl(kern, dim3(grid), dim3(THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<float>(g), g.M, g.N,
+                      (int)((g.K + BK - 1) / BK), mt, nt, g_wait_ns.load());
 }
 
 template <int BN, bool A_MN, bool B_MN>
@@ -757,7 +992,7 @@ cudaError_t split_launch(const GemmArgs& g, int S) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = S > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, maps, epilogue_of(g), g.N, g.M, (int)((g.K + BK - 1) / BK), mt, S,
+    return cudaLaunchKernelEx(&cfg, kern, maps, epilogue_of<bf16>(g), g.N, g.M, (int)((g.K + BK - 1) / BK), mt, S,
                               g_wait_ns.load());
 }
 
@@ -842,6 +1077,15 @@ cudaError_t launch_gemm_tc(const GemmArgs& g) {
         case 64: return lintc::split_layout<64>(g, p.S);
         default: return lintc::split_layout<128>(g, p.S);
     }
+}
+
+cudaError_t launch_gemm_f32(const GemmArgs& g, const F32Planes& f) {
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    if (g.a_mn) return g.b_mn ? lintc::f32_launch<true, true>(g, f, di.sm_count) : cudaErrorInvalidValue;
+    return g.b_mn ? lintc::f32_launch<false, true>(g, f, di.sm_count)
+                  : lintc::f32_launch<false, false>(g, f, di.sm_count);
 }
 
 cudaError_t linear_tc_status(unsigned* out, bool clear) {

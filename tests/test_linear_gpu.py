@@ -167,6 +167,37 @@ def test_non_finite_tokens_stay_in_their_rows(T, K, N, dt):
     _fwd_check(c, "none", (y[keep], z[keep]))
 
 
+@pytest.mark.parametrize("which", ["x", "W", "none"])
+def test_fp32_values_without_bf16_parts(which):
+    # fp32 products of this size are formed from bf16 parts, which infinities, NaN and values next to
+    # fp32's largest do not have: the result is that of fp32 arithmetic all the same
+    T, K, N = 600, 2048, 1030
+    c = _case(T, K, N, F32, 7)
+    if which != "none":
+        c[which][3, 5] = float("inf")
+        c[which][7, K - 1] = -float("inf")
+        c[which][11, 0] = float("nan")
+        c[which][13, 64] = 3.4e38
+    for act in ("none", "relu"):
+        y, z = _fwd(c, act, residual=False)
+        ref = c["x"].double() @ c["W"].double().T + c["bias"].double()
+        got = z.cpu().double()
+        ref32 = ref.float().double()                      # sums past fp32's range are infinite
+        s = c["x"].double().abs() @ c["W"].double().abs().T + c["bias"].double().abs()
+        fin = torch.isfinite(ref32)
+        assert torch.equal(torch.isnan(got), torch.isnan(ref32))
+        assert torch.equal(got[~fin & ~torch.isnan(ref32)], ref32[~fin & ~torch.isnan(ref32)])
+        assert ((got - ref).abs() <= U * ref.abs() + sum_tol(K) * s)[fin].all()
+        keep = ~torch.isnan(ref32)
+        assert torch.equal(y.cpu()[keep], act64(z.cpu(), act)[keep])
+    dx, dW, db = _bwd(c, None, "none")
+    for g, r in ((dx, c["dy"].double() @ c["W"].double()), (dW, c["dy"].double().T @ c["x"].double())):
+        r32 = r.float().double()
+        assert torch.equal(torch.isnan(g.cpu()), torch.isnan(r32))
+        inf = torch.isinf(r32)
+        assert torch.equal(g.cpu().double()[inf], r32[inf])
+
+
 def test_gradient_against_differences():
     # fp64 central differences of the forward's formula confirm the gradients the oracle uses
     c = _case(3, 6, 5, F32, 4)
