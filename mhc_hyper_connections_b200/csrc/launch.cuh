@@ -221,6 +221,9 @@ struct GemmArgs {
 };
 // Where only_if is given, the kernel does nothing unless one of its only_if_n words is set.
 cudaError_t launch_gemm_generic(const GemmArgs& a, const int* only_if = nullptr, int only_if_n = 0);
+// The same for up to 8 rows of A (linear_thin.cu), for products gemm_thin_ok accepts.
+bool gemm_thin_ok(const GemmArgs& a);
+cudaError_t launch_gemm_thin(const GemmArgs& a);
 // The same on the tensor cores (linear_tc.cu), for products gemm_tc_ok accepts: bf16 operands whose
 // rows are 16-byte aligned.
 bool gemm_tc_ok(const GemmArgs& a);

@@ -98,7 +98,7 @@ template <typename T, int BM, int BN, int TM, int TN, bool A_MN, bool B_MN, bool
 __global__ void __launch_bounds__(THREADS)
 gemm_kernel(const T* __restrict__ A, const T* __restrict__ B, int64_t lda, int64_t ldb, int64_t M, int64_t N,
             int64_t K, const float* __restrict__ bias, const T* __restrict__ residual, int act, T* __restrict__ D,
-            T* __restrict__ z, int S, bool veca, bool vecb, const int* __restrict__ only_if, int only_if_n) {
+            T* __restrict__ z, int S, bool veca, bool vecb, bool vecd, const int* __restrict__ only_if, int only_if_n) {
     constexpr int GX = BN / TN;                        // threads along n; THREADS / GX along m
     constexpr int VM = TM < 4 ? TM : 4, VN = 4;        // consecutive rows and columns of a thread
     static_assert(GX * (BM / TM) == THREADS, "threads cover the tile");
@@ -192,9 +192,25 @@ gemm_kernel(const T* __restrict__ A, const T* __restrict__ B, int64_t lda, int64
             const int64_t m = m0 + row(i);
             if (m >= M) continue;
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
+            for (int j = 0; j < TN; j += VN) {
                 const int64_t n = n0 + col(j);
-                if (n < N) finish(kind, m, n, acc[i][j]);
+                if constexpr (sizeof(T) == 4) {
+                    if (vecd) {                        // N a multiple of 4: all four columns, or none
+                        if (n >= N) continue;
+                        float v[4], r[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (residual) Vec16<float>::unpack(ld_stream_v4(residual + m * N + n), r);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = acc[i][j + e] + (bias ? __ldg(bias + n + e) : 0.f);
+                        if (z) st_v4(z + m * N + n, Vec16<float>::pack(v));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = act_value<kind(), false>(v[e]) + r[e];
+                        st_v4(D + m * N + n, Vec16<float>::pack(v));
+                        continue;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < VN; ++e)
+                    if (n + e < N) finish(kind, m, n + e, acc[i][j + e]);
             }
         }
     });
@@ -220,7 +236,8 @@ cudaError_t launch(const GemmArgs& g, int S, const int* only_if, int only_if_n) 
     return cudaLaunchKernelEx(&cfg, gemm_kernel<T, BM, BN, TM, TN, A_MN, B_MN, ONLY_IF>, static_cast<const T*>(g.A),
                               static_cast<const T*>(g.B), g.lda, g.ldb, g.M, g.N, g.K, g.bias,
                               static_cast<const T*>(g.residual), (int)g.act, static_cast<T*>(g.D),
-                              static_cast<T*>(g.z), S, vec(g.A, g.lda), vec(g.B, g.ldb), only_if, only_if_n);
+                              static_cast<T*>(g.z), S, vec(g.A, g.lda), vec(g.B, g.ldb),
+                              vec(g.D, g.N) && vec(g.z, g.N) && vec(g.residual, g.N), only_if, only_if_n);
 }
 
 template <typename T, bool A_MN, bool B_MN>
