@@ -457,6 +457,19 @@ mhc_status mhc_debug_pre_stop_after(int32_t tiles, uint32_t wait_limit_us);
  */
 mhc_status mhc_debug_backward_stop_after(int32_t stages, uint32_t wait_limit_us);
 
+/*
+ * mhc_debug_sublayer_stop_after -- test hook for the failure path of the sub-layer operators: the
+ * tensor-core products of mhc_linear and mhc_linear_backward, and the layer norm kernels that
+ * bring rows into shared memory (16-byte-aligned rows, more of them than SMs).  After this call
+ * their launches stop loading after `stages` stages per CTA, or batches of rows per ring
+ * (stages < 0: never, the default), and give up a wait after `wait_limit_us` microseconds
+ * (default 1000000; accepted range 1000 .. 10000000, else MHC_ERR_SHAPE).  The waits for what is
+ * never loaded run into their limit, the kernels set bits 29-31 in mhc_device_status, let their
+ * copies and MMAs in flight complete and return with their outputs incomplete.  Process-wide,
+ * from the next launch.
+ */
+mhc_status mhc_debug_sublayer_stop_after(int32_t stages, uint32_t wait_limit_us);
+
 /* Static English text for a status code (never NULL). */
 const char* mhc_status_string(mhc_status status);
 

@@ -39,7 +39,7 @@ __all__ = ["mhc_pre", "mhc_pre_with_path", "mhc_pre_hc", "mhc_pre_train", "mhc_p
            "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU",
            "mhc_amax_gain", "mhc_pre_path_for", "mhc_pre_path_ok", "mhc_device_status",
            "mhc_debug_pre_stop_after", "mhc_debug_backward_stop_after",
-           "MhcError",
+           "mhc_debug_sublayer_stop_after", "MhcError",
            "MHC_F32", "MHC_BF16", "PRE_AUTO", "PRE_GENERIC", "PRE_CLUSTER_TC", "PRE_TWO_PASS_TC", "library_path",
            "load_library", "EXPORTED_SYMBOLS"]
 
@@ -63,7 +63,7 @@ EXPORTED_SYMBOLS = ("mhc_pre", "mhc_pre_with_path", "mhc_pre_hc", "mhc_pre_train
                     "mhc_linear_backward_workspace_bytes", "mhc_linear_backward",
                     "mhc_amax_gain", "mhc_status_string",
                     "mhc_last_error", "mhc_device_status", "mhc_debug_pre_stop_after",
-                    "mhc_debug_backward_stop_after")
+                    "mhc_debug_backward_stop_after", "mhc_debug_sublayer_stop_after")
 
 _lock = threading.Lock()
 _lib = None
@@ -146,6 +146,8 @@ def load_library():
         lib.mhc_debug_pre_stop_after.restype = ci
         lib.mhc_debug_backward_stop_after.argtypes = [ctypes.c_int32, ctypes.c_uint32]
         lib.mhc_debug_backward_stop_after.restype = ci
+        lib.mhc_debug_sublayer_stop_after.argtypes = [ctypes.c_int32, ctypes.c_uint32]
+        lib.mhc_debug_sublayer_stop_after.restype = ci
         _lib = lib
     return _lib
 
@@ -645,6 +647,15 @@ def mhc_debug_backward_stop_after(stages: int, wait_limit_us: int = 1_000_000) -
     a wait after `wait_limit_us` microseconds; mhc_device_status() then reports bits 24-28."""
     _check(load_library().mhc_debug_backward_stop_after(int(stages), int(wait_limit_us)),
            "mhc_debug_backward_stop_after")
+
+
+def mhc_debug_sublayer_stop_after(stages: int, wait_limit_us: int = 1_000_000) -> None:
+    """Test hook of the sub-layer operators' failure path: later launches of the tensor-core
+    products and of the layer norm kernels that load through shared memory stop loading after
+    `stages` stages per CTA (stages < 0 restores normal operation) and give up a wait after
+    `wait_limit_us` microseconds; mhc_device_status() then reports bits 29-31."""
+    _check(load_library().mhc_debug_sublayer_stop_after(int(stages), int(wait_limit_us)),
+           "mhc_debug_sublayer_stop_after")
 
 
 def mhc_pre_path_ok(T: int, n: int, d: int, dtype, path: int) -> bool:

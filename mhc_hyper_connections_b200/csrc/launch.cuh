@@ -175,6 +175,9 @@ int64_t layer_norm_part_floats(int64_t T, int d);
 cudaError_t launch_layer_norm(const LnArgs& a);
 cudaError_t launch_layer_norm_backward(const LnArgs& a);
 cudaError_t layer_norm_status(unsigned* out, bool clear);
+// Failure-path test hook: launches after this call stop loading after `stop` batches per ring (< 0:
+// never) and give up a wait after `wait_ns`.
+void layer_norm_set_stop(int stop, unsigned long long wait_ns);
 
 // The linear product with its epilogue, forward and backward (linear.cu).
 enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
@@ -237,6 +240,7 @@ struct F32Planes {
 };
 cudaError_t launch_gemm_f32(const GemmArgs& a, const F32Planes& f);
 cudaError_t linear_tc_status(unsigned* out, bool clear);
+void linear_tc_set_stop(int stop, unsigned long long wait_ns);      // as layer_norm_set_stop, in stages per CTA
 
 // Amax Gain Magnitude of composite residual maps (diagnostics.cu).
 cudaError_t launch_amax_gain(const float* Hs, int L, int64_t T, int n, float* gain, cudaStream_t s);

@@ -23,6 +23,8 @@
 //   * long kernels, for rows beyond the registers of a block: three walks over the row.
 // Column sums are added up in a fixed order: over a group's rows, over a block's warps in shared
 // memory, and over the blocks by a second kernel that reads one fp32 row pair per block.
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.cuh"
 #include "tc_ptx.cuh"
@@ -378,12 +380,12 @@ ln_bwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
 
 constexpr int MAX_SLOTS = 8;
 constexpr int WARP_SLOTS = 4;            // of a warp's own ring
-constexpr unsigned long long kRingWaitNs = 1000000000ull;    // 1 s per wait
 constexpr unsigned long long kRingLandNs = 2000000ull;       // after a failed wait: copies in flight land
 
 // A wait that expires sets the status word and the block's abort flag; after it no wait blocks, the
 // loops run out and the outputs are incomplete.
-__device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           unsigned long long limit_ns) {
     for (int i = 0; i < 256; ++i) {
         if (ptx::mbar_try(bar, parity)) return true;
         if (*abort_flag) return false;
@@ -392,7 +394,7 @@ __device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, volati
     while (true) {
         if (ptx::mbar_try(bar, parity)) return true;
         if (*abort_flag) return false;
-        if (ptx::gtimer() - t0 > kRingWaitNs) {
+        if (ptx::gtimer() - t0 > limit_ns) {
             atomicOr(&g_layer_norm_status, 1u);
             *abort_flag = 1;
             return false;
@@ -404,11 +406,18 @@ __device__ __forceinline__ void land() {
     while (ptx::gtimer() - t0 < kRingLandNs) __nanosleep(1000);
 }
 
+// The wait limit, and the failure-path test hook: batches after which loading stops (< 0: never)
+struct Limits {
+    unsigned long long wait_ns;
+    int stop;
+};
+
 // A ring of slots filled by the producer warp.
 struct Ring {
     uint64_t* bars;                      // [2 MAX_SLOTS]: full, empty
     volatile int* abort_flag;
     int slots;
+    Limits lim;
     int s = 0;
     uint32_t parity = 0;
 
@@ -420,7 +429,7 @@ struct Ring {
             parity ^= 1u;
         }
     }
-    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t par) const { return wait_until(bar, par, abort_flag); }
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t par) const { return wait_until(bar, par, abort_flag, lim.wait_ns); }
 };
 
 // set up by thread 0; the caller synchronises the block
@@ -439,7 +448,8 @@ __device__ __forceinline__ void ring_produce(Ring ring, unsigned char* smem, con
                                              int64_t Tn, int B, int64_t row_bytes, int64_t batches) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
-        for (int64_t i = blockIdx.x; i < batches; i += gridDim.x, ring.next()) {
+        int left = ring.lim.stop;
+        for (int64_t i = blockIdx.x; i < batches && left != 0; i += gridDim.x, ring.next(), --left) {
             if (!(ok = ring.wait(ring.empty(), ring.parity ^ 1u))) break;
             const int64_t row = i * B;
             const uint32_t bytes = (uint32_t)((Tn - row < B ? Tn - row : B) * row_bytes);
@@ -494,7 +504,8 @@ __device__ __forceinline__ void load_columns(const float* __restrict__ p, int d,
 template <typename T, int NV, int R, int G, int TH>
 __global__ void __launch_bounds__(TH + 32)
 ln_fwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int64_t Tn, int d,
-                   float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots) {
+                   float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots,
+                   Limits lim) {
     constexpr int VEC = Vec16<T>::VEC, HV = VEC / 2;
     constexpr int B = G ? WARPS * (32 / (G ? G : 32)) * R : R;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -507,7 +518,7 @@ ln_fwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
     __syncthreads();
     pdl_launch_next();
     pdl_wait();
-    Ring ring{bars, &abort_flag, slots};
+    Ring ring{bars, &abort_flag, slots, lim};
     const int64_t batches = (Tn + B - 1) / B, row_bytes = (int64_t)d * sizeof(T);
     if (warp == consumers >> 5) {
         const unsigned char* const src[1] = {reinterpret_cast<const unsigned char*>(x)};
@@ -602,7 +613,8 @@ template <int NV> constexpr int WARP_BLOCKS = NV > 10 ? 1 : NV > 8 ? 2 : NV > 4 
 template <typename T, int NV>
 __global__ void __launch_bounds__(256, WARP_BLOCKS<NV>)
 ln_fwd_warp_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int64_t Tn, int d,
-                   float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots) {
+                   float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots,
+                   Limits lim) {
     constexpr int TH = 256;
     constexpr int VEC = Vec16<T>::VEC, HV = VEC / 2, PL = VEC / 4;
     extern __shared__ float4 wb[];      // [w, b][NV][PL][32], then the warps' slots
@@ -619,7 +631,10 @@ ln_fwd_warp_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
     const int64_t warps = (int64_t)gridDim.x * (TH / 32);
     int64_t row = (int64_t)warp * gridDim.x + blockIdx.x;      // the last, partial round goes to all blocks
     unsigned char* ring = reinterpret_cast<unsigned char*>(wb + 2 * NV * PL * 32) + (size_t)warp * slots * row_bytes;
+    int left = lim.stop;
     auto load = [&](int64_t r, int s) {
+        if (left == 0) return;
+        --left;
         const uint32_t bar = ptx::smem_u32(&bars[warp][s]);
         ptx::mbar_arrive_tx(bar, row_bytes);
         ptx::bulk_g2s(ptx::smem_u32(ring) + s * row_bytes, x + r * d, row_bytes, bar);
@@ -644,7 +659,7 @@ ln_fwd_warp_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
     __syncthreads();
     const float inv_d = 1.0f / (float)d;
     for (; row < Tn; row += warps) {
-        ok = wait_until(ptx::smem_u32(&bars[warp][slot]), parity, &abort_flag) && ok;
+        ok = wait_until(ptx::smem_u32(&bars[warp][slot]), parity, &abort_flag, lim.wait_ns) && ok;
         uint4 raw[NV];
         const T* xr = reinterpret_cast<const T*>(ring + (size_t)slot * row_bytes) + lane * VEC;
 #pragma unroll
@@ -717,7 +732,7 @@ template <typename T, int NV, int R, int G, int TH>
 __global__ void __launch_bounds__(TH + 32, 1)
 ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
                    const float* __restrict__ rstd, const T* __restrict__ dy, int64_t Tn, int d, T* __restrict__ dx,
-                   float* __restrict__ part, int slots) {
+                   float* __restrict__ part, int slots, Limits lim) {
     constexpr int VEC = Vec16<T>::VEC, HV = VEC / 2;
     constexpr int GROUPS = G ? WARPS * (32 / (G ? G : 32)) : 1, B = GROUPS * R;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -730,7 +745,7 @@ ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
     __syncthreads();
     pdl_launch_next();
     pdl_wait();
-    Ring ring{bars, &abort_flag, slots};
+    Ring ring{bars, &abort_flag, slots, lim};
     const int64_t batches = (Tn + B - 1) / B, row_bytes = (int64_t)d * sizeof(T);
     if (warp == consumers >> 5) {
         const unsigned char* const src[2] = {reinterpret_cast<const unsigned char*>(x),
@@ -946,6 +961,11 @@ cudaError_t bwd(const LnArgs& a, int* blocks) {
                       a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part);
 }
 
+std::atomic<unsigned long long> g_wait_ns{1000000000ull};      // 1 s per wait
+std::atomic<int> g_stop{-1};
+
+Limits limits() { return Limits{g_wait_ns.load(), g_stop.load()}; }
+
 // Launch shape of a ring kernel: threads, rows per slot, and slots.  The SM's shared memory goes to
 // about 640 threads' worth of blocks.
 struct RingShape {
@@ -979,7 +999,7 @@ cudaError_t fwd_ring(const LnArgs& a) {
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3((unsigned)(want < cap ? want : cap)), dim3(r.threads), r.bytes, a.stream,
                       static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd,
-                      r.slots);
+                      r.slots, limits());
 }
 
 template <typename T, int NV, int R, int G, int TH>
@@ -997,7 +1017,7 @@ cudaError_t bwd_ring(const LnArgs& a, int* blocks) {
     *blocks = (int)(want < cap ? want : cap);
     return launch_pdl(kern, dim3((unsigned)*blocks), dim3(r.threads), r.bytes, a.stream, static_cast<const T*>(a.x),
                       a.w, a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part,
-                      r.slots);
+                      r.slots, limits());
 }
 
 template <typename T, int NV>
@@ -1016,7 +1036,8 @@ cudaError_t fwd_warp(const LnArgs& a) {
     e = resident(kern, TH, smem, want, &cap);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3((unsigned)(want < cap ? want : cap)), dim3(TH), smem, a.stream,
-                      static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd, slots);
+                      static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd, slots,
+                      limits());
 }
 
 // The layout of a row by its length in vectors: 8, 16 or 32 lanes with one vector each, 32 with two,
@@ -1107,6 +1128,11 @@ cudaError_t launch_layer_norm_backward(const LnArgs& a) {
     if (e != cudaSuccess || !a.part) return e;
     const unsigned grid = (unsigned)((2 * (int64_t)a.d + 31) / 32);
     return launch_pdl(ln_cols_kernel, dim3(grid), dim3(512), 0, a.stream, a.part, blocks, a.d, a.dw, a.db);
+}
+
+void layer_norm_set_stop(int stop, unsigned long long wait_ns) {
+    g_stop.store(stop);
+    g_wait_ns.store(wait_ns);
 }
 
 cudaError_t layer_norm_status(unsigned* out, bool clear) {

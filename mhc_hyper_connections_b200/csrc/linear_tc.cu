@@ -183,6 +183,12 @@ struct Maps {
     CUtensorMap a, b;
 };
 
+// The wait limit, and the failure-path test hook: stages after which a CTA stops loading (< 0: never)
+struct Limits {
+    unsigned long long wait_ns;
+    int stop;
+};
+
 template <typename T>
 struct Epilogue {
     const float* bias;
@@ -296,7 +302,7 @@ __device__ __forceinline__ void tile_at(int64_t i, int mt, int nt, int& m, int& 
 template <int BN, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<bf16> ep, int64_t M, int64_t N, int kblocks, int mt,
-                 int nt, unsigned long long wait_ns) {
+                 int nt, Limits lim) {
     using C = PairCfg<BN>;
     constexpr int NS = C::NS, KS = C::KS;
     extern __shared__ unsigned char smem_raw[];
@@ -309,8 +315,8 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
     auto accf = [&](int b) { return smem_u32(&bars[2 * NS + b]); };  // accumulator complete
     auto acce = [&](int b) { return smem_u32(&bars[2 * NS + 2 + b]); };   // first CTA: read by both CTAs
     const uint32_t drained = smem_u32(&bars[2 * NS + 4]);
-    const Waiter wait{&abort_flag, wait_ns};
-    const Waiter drain{&abort_flag, wait_ns > kDrainNs ? wait_ns : kDrainNs};
+    const Waiter wait{&abort_flag, lim.wait_ns};
+    const Waiter drain{&abort_flag, lim.wait_ns > kDrainNs ? lim.wait_ns : kDrainNs};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank(), base = smem_u32(sm);
 
@@ -343,11 +349,12 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
     if (warp == 0) {
         Ring<NS> ring;
         bool ok = true;
-        for (int64_t i = first; ok && i < tiles; i += stride) {
+        int left = lim.stop;
+        for (int64_t i = first; ok && left != 0 && i < tiles; i += stride) {
             int m, n;
             tile_at(i, mt, nt, m, n);
             const int m0 = m * 256 + (int)rank * 128, n0 = n * BN + (int)rank * (BN / 2);
-            for (int kb = 0; kb < kblocks; kb += KS, ring.next()) {
+            for (int kb = 0; kb < kblocks && left != 0; kb += KS, ring.next(), --left) {
                 const int s = ring.s;
                 if (!(ok = wait.warp(empty(s), ring.parity ^ 1u, E_STAGE))) break;
                 if (elect_one()) {
@@ -484,7 +491,7 @@ struct F32Cfg {
 template <bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<float> ep, int64_t M, int64_t N,
-                int kblocks, int mt, int nt, unsigned long long wait_ns) {
+                int kblocks, int mt, int nt, Limits lim) {
     using C = F32Cfg;
     constexpr int NS = C::NS, BN = C::BN;
     extern __shared__ unsigned char smem_raw[];
@@ -497,8 +504,8 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
     auto accf = [&](int b) { return smem_u32(&bars[2 * NS + b]); };
     auto acce = [&](int b) { return smem_u32(&bars[2 * NS + 2 + b]); };
     const uint32_t drained = smem_u32(&bars[2 * NS + 4]);
-    const Waiter wait{&abort_flag, wait_ns};
-    const Waiter drain{&abort_flag, wait_ns > kDrainNs ? wait_ns : kDrainNs};
+    const Waiter wait{&abort_flag, lim.wait_ns};
+    const Waiter drain{&abort_flag, lim.wait_ns > kDrainNs ? lim.wait_ns : kDrainNs};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank(), base = smem_u32(sm);
 
@@ -529,11 +536,12 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
     if (warp == 0) {
         Ring<NS> ring;
         bool ok = true;
-        for (int64_t i = first; ok && i < tiles; i += stride) {
+        int left = lim.stop;
+        for (int64_t i = first; ok && left != 0 && i < tiles; i += stride) {
             int m, n;
             tile_at(i, mt, nt, m, n);
             const int m0 = m * 256 + (int)rank * 128, n0 = n * BN + (int)rank * (BN / 2);
-            for (int kb = 0; kb < kblocks; ++kb, ring.next()) {
+            for (int kb = 0; kb < kblocks && left != 0; ++kb, ring.next(), --left) {
                 const int s = ring.s;
                 if (!(ok = wait.warp(empty(s), ring.parity ^ 1u, E_STAGE))) break;
                 if (elect_one()) {
@@ -668,7 +676,7 @@ struct SplitCfg {
 template <int BN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(THREADS, SplitCfg<BN>::PER_SM)
 gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<bf16> ep, int64_t Mr, int64_t Nc, int kblocks, int mt,
-                  int S, unsigned long long wait_ns) {
+                  int S, Limits lim) {
     using C = SplitCfg<BN>;
     constexpr int NS = C::NS, KS = C::KS;
     extern __shared__ unsigned char smem_raw[];
@@ -679,8 +687,8 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
     auto full = [&](int s) { return smem_u32(&bars[s]); };
     auto empty = [&](int s) { return smem_u32(&bars[NS + s]); };
     const uint32_t accf = smem_u32(&bars[2 * NS]), drained = smem_u32(&bars[2 * NS + 1]);
-    const Waiter wait{&abort_flag, wait_ns};
-    const Waiter drain{&abort_flag, wait_ns > kDrainNs ? wait_ns : kDrainNs};
+    const Waiter wait{&abort_flag, lim.wait_ns};
+    const Waiter drain{&abort_flag, lim.wait_ns > kDrainNs ? lim.wait_ns : kDrainNs};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
     const uint32_t base = smem_u32(sm);
@@ -719,7 +727,8 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
     if (warp == 0) {
         Ring<NS> ring;
         bool ok = true;
-        for (int kb = k_lo; kb < k_hi; kb += KS, ring.next()) {
+        int left = lim.stop;
+        for (int kb = k_lo; kb < k_hi && left != 0; kb += KS, ring.next(), --left) {
             const int s = ring.s;
             if (!(ok = wait.warp(empty(s), ring.parity ^ 1u, E_STAGE))) break;
             if (elect_one()) {
@@ -909,6 +918,9 @@ bool make_map_planes(CUtensorMap* map, const void* p, int64_t rows, int64_t K, i
 }
 
 std::atomic<unsigned long long> g_wait_ns{kWaitNs};
+std::atomic<int> g_stop{-1};
+
+Limits limits() { return Limits{g_wait_ns.load(), g_stop.load()}; }
 
 template <typename K>
 cudaError_t allow_smem(K kern, int bytes) {
@@ -941,7 +953,7 @@ cudaError_t pair_launch(const GemmArgs& g, int sms) {
     const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
     return launch_pdl(kern, dim3(grid), dim3(THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<bf16>(g), g.M, g.N,
-                      (int)((g.K + BK - 1) / BK), mt, nt, g_wait_ns.load());
+                      (int)((g.K + BK - 1) / BK), mt, nt, limits());
 }
 
 template <int BN>
@@ -964,7 +976,7 @@ cudaError_t f32_launch(const GemmArgs& g, const F32Planes& f, int sms) {
     const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
     return launch_pdl(kern, dim3(grid), dim3(THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<float>(g), g.M, g.N,
-                      (int)((g.K + BK - 1) / BK), mt, nt, g_wait_ns.load());
+                      (int)((g.K + BK - 1) / BK), mt, nt, limits());
 }
 
 template <int BN, bool A_MN, bool B_MN>
@@ -993,7 +1005,7 @@ cudaError_t split_launch(const GemmArgs& g, int S) {
     cfg.attrs = at;
     cfg.numAttrs = S > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, maps, epilogue_of<bf16>(g), g.N, g.M, (int)((g.K + BK - 1) / BK), mt, S,
-                              g_wait_ns.load());
+                              limits());
 }
 
 template <int BN>
@@ -1086,6 +1098,11 @@ cudaError_t launch_gemm_f32(const GemmArgs& g, const F32Planes& f) {
     if (g.a_mn) return g.b_mn ? lintc::f32_launch<true, true>(g, f, di.sm_count) : cudaErrorInvalidValue;
     return g.b_mn ? lintc::f32_launch<false, true>(g, f, di.sm_count)
                   : lintc::f32_launch<false, false>(g, f, di.sm_count);
+}
+
+void linear_tc_set_stop(int stop, unsigned long long wait_ns) {
+    lintc::g_stop.store(stop);
+    lintc::g_wait_ns.store(wait_ns);
 }
 
 cudaError_t linear_tc_status(unsigned* out, bool clear) {

@@ -188,4 +188,12 @@ mhc_status mhc_linear_backward(const void* x, const void* W, const void* z, int6
     return e == cudaSuccess ? MHC_OK : report_cuda_error(e, "mhc_linear_backward");
 }
 
+mhc_status mhc_debug_sublayer_stop_after(int32_t stages, uint32_t wait_limit_us) {
+    if (wait_limit_us < 1000u || wait_limit_us > 10000000u) return MHC_ERR_SHAPE;
+    const int stop = stages < 0 ? -1 : (int)stages;
+    layer_norm_set_stop(stop, (unsigned long long)wait_limit_us * 1000ull);
+    linear_tc_set_stop(stop, (unsigned long long)wait_limit_us * 1000ull);
+    return MHC_OK;
+}
+
 }  // extern "C"

@@ -90,6 +90,12 @@ def test_linear_backward_validation(lib):
     assert linb(T=0, dW=P[5] + 1) == 3 and linb(T=0, db=P[5]) == 7
 
 
+def test_stop_hook_validation(lib):
+    assert lib.mhc_debug_sublayer_stop_after(-1, 999) == 2
+    assert lib.mhc_debug_sublayer_stop_after(3, 10_000_001) == 2
+    assert lib.mhc_debug_sublayer_stop_after(-1, 1_000_000) == 0
+
+
 # ---- the binding
 
 def _t(*shape, dtype=torch.bfloat16):
