@@ -646,6 +646,81 @@ def run_amax(args, rank, world, local_rank):
         print(json.dumps(line), flush=True)
 
 
+def run_ffn(args, rank, world, local_rank):
+    """A training step of an mHC-wrapped feed-forward layer at the workload's T, n, d with 4 d
+    hidden channels: pre, layer norm, up projection with GELU, down projection, post, and the
+    backward of all of them.  Prints one JSON line."""
+    import torch
+
+    import mhc_hyper_connections_b200 as mhc
+    from mhc_hyper_connections_b200 import dist as mdist
+    from mhc_hyper_connections_b200 import workloads as wl
+
+    torch.cuda.set_device(local_rank)
+    dev = torch.device("cuda", local_rank)
+    w = wl.make_config(args.config)
+    T, n, d, m, hid = args.tokens or w.T, w.n, w.d, w.m, 4 * w.d
+    dt = torch.bfloat16 if w.dtype == "bf16" else torch.float32
+    g = torch.Generator(device=dev)
+    g.manual_seed(1234 + rank)
+    r = lambda *s: torch.randn(*s, generator=g, device=dev)
+    e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device=dev)
+    X, dY = r(T, n, d).to(dt), r(T, n, d).to(dt)
+    phi, b_res = r(n * d, m) * (n * d) ** -0.5, 4 * torch.eye(n, device=dev)
+    zero = torch.zeros(n, device=dev)
+    pre = (phi, zero, zero, b_res, w.alpha_pre, w.alpha_post, w.alpha_res, w.eps, w.t_max)
+    lw, lb, c1, c2 = 1 + 0.1 * r(d), 0.1 * r(d), 0.1 * r(hid), 0.1 * r(d)
+    W1, W2 = (r(hid, d) * d ** -0.5).to(dt), (r(d, hid) * hid ** -0.5).to(dt)
+    x_in, xn, F, dF, dxn, dx = (e(T, d, dtype=dt) for _ in range(6))
+    H, h, mean, rstd = e(T, m), e(T, m), e(T), e(T)
+    u, z, du = (e(T, hid, dtype=dt) for _ in range(3))
+    Y, dX = torch.empty_like(X), torch.empty_like(X)
+    dW1, dW2, dlw, dlb, dc1, dc2 = (torch.empty_like(t) for t in (W1, W2, lw, lb, c1, c2))
+    dphi, dbp, dbq, dbr, dal = e(n * d, m), e(n), e(n), e(n, n), e(3)
+    no_dx = torch.zeros_like(x_in)
+    ws = lambda b: torch.empty(max(int(b), 1), dtype=torch.uint8, device=dev)
+    w_lin = ws(max(mhc.mhc_linear_workspace_bytes(T, d, hid, dt), mhc.mhc_linear_workspace_bytes(T, hid, d, dt)))
+    w_back = ws(max(mhc.mhc_linear_backward_workspace_bytes(T, d, hid, dt),
+                    mhc.mhc_linear_backward_workspace_bytes(T, hid, d, dt)))
+    w_norm, w_mhc = ws(mhc.mhc_layer_norm_backward_workspace_bytes(T, d)), ws(mhc.mhc_backward_workspace_bytes(T, n, d))
+
+    def back(dx_in):
+        mhc.mhc_backward(X, F, *pre, H, h, dY, dx_in, dX, dF, dphi, dbp, dbq, dbr, dal, w_mhc)
+
+    def step():
+        mhc.mhc_pre_train(X, *pre, x_in, H, h)
+        mhc.mhc_layer_norm(x_in, lw, lb, 1e-5, xn, mean, rstd)
+        mhc.mhc_linear(xn, W1, c1, u, act=mhc.ACT_GELU, z=z, workspace=w_lin)
+        mhc.mhc_linear(u, W2, c2, F, workspace=w_lin)
+        mhc.mhc_post(X, F, H, Y)
+        back(no_dx)                      # dF_out, which the sub-layer's backward starts from
+        mhc.mhc_linear_backward(u, W2, None, dF, du, dW2, dc2, w_back)
+        mhc.mhc_linear_backward(xn, W1, z, du, dxn, dW1, dc1, w_back, act=mhc.ACT_GELU)
+        mhc.mhc_layer_norm_backward(x_in, lw, mean, rstd, dxn, dx, dlw, dlb, w_norm)
+        back(dx)
+
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize()
+    K = args.steps
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(K):
+        step()
+    b.record()
+    torch.cuda.synchronize()
+    assert mhc.mhc_device_status() == 0
+    ms = mdist.max_over_ranks(a.elapsed_time(b), device=dev)
+    flops = 12 * T * d * hid
+    line = {"metric": "mHC-wrapped feed-forward layer, training step: tokens/s", "value": T * K * world / (ms / 1e3),
+            "unit": "tokens/s", "n_gpus": world, "steps": K, "warmup": args.warmup, "ms_per_step": ms / K,
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": w.dtype, "data": "synthetic",
+            "config": {"workload": f"ffn_T{T}_n{n}_d{d}_hidden{hid}", "T": T, "n": n, "d": d, "hidden": hid},
+            "linear_tflops": flops / (ms / 1e3 / K) / 1e12}
+    if rank == 0:
+        print(json.dumps(line), flush=True)
+
+
 def main():
     from mhc_hyper_connections_b200 import workloads as wl
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
@@ -669,6 +744,8 @@ def main():
                     help="time the composite Amax gain diagnostic (mhc_amax_gain, 60 layers)")
     ap.add_argument("--backward", action="store_true",
                     help="time forward + backward steps (mhc_pre_train, mhc_post, mhc_backward)")
+    ap.add_argument("--ffn", action="store_true",
+                    help="time training steps of an mHC-wrapped feed-forward layer (4 d hidden channels)")
     args = ap.parse_args()
     if args.warmup < 3:
         ap.error("--warmup must be >= 3")
@@ -682,6 +759,8 @@ def main():
         return run_reference(args, rank, world)
     if args.backward:
         return run_backward(args, rank, world, local_rank)
+    if args.ffn:
+        return run_ffn(args, rank, world, local_rank)
     if args.amax:
         return run_amax(args, rank, world, local_rank)
     return run_ours(args, rank, world, local_rank)
