@@ -23,9 +23,23 @@ constexpr float kInvSqrt2Pi = 0.39894228040143267794f;    // 1 / sqrt(2 pi)
 constexpr float kSqrt8OverPi = 1.59576912160573071176f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// the hardware's 2^x and 1 / x
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <bool FAST>
 __device__ __forceinline__ float act_sigmoid(float z) {
-    if constexpr (FAST) return __fdividef(1.0f, 1.0f + __expf(-z));
+    if constexpr (FAST) return rcp_approx(1.0f + ex2_approx(-kLog2e * z));
     return sigmoid_f32(z);
 }
 
@@ -33,16 +47,16 @@ __device__ __forceinline__ float act_sigmoid(float z) {
 template <bool FAST>
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
     if constexpr (FAST) {
-        e = __expf(-0.5f * z * z);
-        const float t = __fdividef(1.0f, fmaf(0.38f * kSqrtHalf, fabsf(z), 1.0f));
-        float p = -0.12520070f;
-        p = fmaf(p, t, 0.33520198f);
-        p = fmaf(p, t, -0.06861920f);
-        p = fmaf(p, t, 0.24680305f);
-        p = fmaf(p, t, 0.18103781f);
-        p = fmaf(p, t, 0.21648033f);
-        p = fmaf(p, t, 0.21429573f);
-        const float tail = 0.5f * t * p * e;               // Phi(-|z|)
+        e = ex2_approx((-0.5f * kLog2e * z) * z);
+        const float t = rcp_approx(fmaf(0.38f * kSqrtHalf, fabsf(z), 1.0f));
+        float p = 0.5f * -0.12520070f;                     // P / 2
+        p = fmaf(p, t, 0.5f * 0.33520198f);
+        p = fmaf(p, t, 0.5f * -0.06861920f);
+        p = fmaf(p, t, 0.5f * 0.24680305f);
+        p = fmaf(p, t, 0.5f * 0.18103781f);
+        p = fmaf(p, t, 0.5f * 0.21648033f);
+        p = fmaf(p, t, 0.5f * 0.21429573f);
+        const float tail = t * p * e;                      // Phi(-|z|)
         return z > 0.f ? 1.0f - tail : tail;
     } else {
         e = expf(-0.5f * z * z);

@@ -18,7 +18,7 @@ namespace {
 
 constexpr int DZ_COLS = 32;            // threads along a row
 constexpr int DZ_ROWS = 8;             // rows a block takes at a time
-constexpr int DZ_BLOCKS = 8 * 148;     // blocks wanted, eight per SM of a 148-SM device
+constexpr int DZ_BLOCKS = 16 * 148;    // blocks wanted, sixteen per SM of a 148-SM device
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
@@ -41,13 +41,13 @@ __device__ __forceinline__ void dz_load(const T* __restrict__ p, int64_t t, int6
     }
 }
 
-// A thread takes VEC columns and four tokens at a time (their loads are in flight together).  dz
-// null: column sums only; part null: no sums.
+// A thread takes VEC columns of a token at a time: its two loads, and many blocks per SM in place of
+// more of them (T = N = 16384 with GELU: four tokens at a time took 540 us, one 325).  dz null: column
+// sums only; part null: no sums.
 template <typename T, int VEC, int ACT, bool SHIFT>
 __global__ void __launch_bounds__(DZ_COLS* DZ_ROWS)
 dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, int64_t run, T* __restrict__ dz,
           int64_t ld, float* __restrict__ part) {
-    constexpr int U = 4;
     __shared__ float sm[DZ_ROWS][DZ_COLS * VEC + 1];
     pdl_launch_next();
     pdl_wait();
@@ -56,32 +56,21 @@ dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, 
     const int64_t t0 = (int64_t)blockIdx.y * run, t1 = t0 + run < Tn ? t0 + run : Tn;
     float s[VEC] = {};
     if (c < N) {
-        for (int64_t t = t0 + ty; t < t1; t += DZ_ROWS * U) {
-            float g[U][VEC], zf[U][VEC];
+        for (int64_t t = t0 + ty; t < t1; t += DZ_ROWS) {
+            float g[VEC], zf[VEC];
+            dz_load<T, VEC, SHIFT>(dy, t, c, Tn, N, g);
+            if constexpr (ACT != ACT_NONE) dz_load<T, VEC, SHIFT>(z, t, c, Tn, N, zf);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t tu = t + u * DZ_ROWS;
-                if (tu >= t1) break;
-                dz_load<T, VEC, SHIFT>(dy, tu, c, Tn, N, g[u]);
-                if constexpr (ACT != ACT_NONE) dz_load<T, VEC, SHIFT>(z, tu, c, Tn, N, zf[u]);
+            for (int e = 0; e < VEC; ++e) {
+                // rounded as a product whether or not dz is stored, so that the sums are the same bits
+                if constexpr (ACT != ACT_NONE) g[e] = __fmul_rn(g[e], act_slope<ACT, sizeof(T) == 2>(zf[e]));
+                s[e] += g[e];
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t tu = t + u * DZ_ROWS;
-                if (tu >= t1) break;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    // rounded as a product whether or not dz is stored, so that the sums are the same bits
-                    if constexpr (ACT != ACT_NONE)
-                        g[u][e] = __fmul_rn(g[u][e], act_slope<ACT, sizeof(T) == 2>(zf[u][e]));
-                    s[e] += g[u][e];
-                }
-                if (dz) {
-                    if constexpr (VEC > 1) {
-                        st_v4(dz + tu * ld + c, Vec16<T>::pack(g[u]));      // may fill up the row's padding
-                    } else {
-                        store_elem(dz + tu * ld + c, g[u][0]);
-                    }
+            if (dz) {
+                if constexpr (VEC > 1) {
+                    st_v4(dz + t * ld + c, Vec16<T>::pack(g));      // may fill up the row's padding
+                } else {
+                    store_elem(dz + t * ld + c, g[0]);
                 }
             }
         }

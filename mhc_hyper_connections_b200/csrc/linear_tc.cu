@@ -199,6 +199,16 @@ struct Epilogue {
     int vec;                             // rows of D, z and residual are 16-byte aligned
 };
 
+// A warp's 32 rows x `cols` columns of the residual on their way to L2, while their tile is formed (a row
+// per lane; T = 4096, 1024 -> 4096 with a residual from HBM: see finish_block's loads)
+template <typename T>
+__device__ __forceinline__ void prefetch_residual(const Epilogue<T>& ep, int64_t r0, int64_t c0, int cols, int64_t M,
+                                                  int64_t N, int lane) {
+    if (!ep.residual || r0 + lane >= M) return;
+    for (int c = 0; c < cols && c0 + c < N; c += ROW / (int)sizeof(T))
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(ep.residual + (r0 + lane) * N + c0 + c));
+}
+
 // The outputs of a warp's 32 rows x 128 bytes of columns at (r0, c0) from their sums, a row per lane:
 // v = act(v + bias) + residual, and z.  Between registers and memory (128 bytes of a row per eight
 // lanes) the block goes through the warp's 4 KB of shared memory, swizzled by 16-byte chunks.
@@ -207,17 +217,18 @@ __device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[R
                                              int64_t r0, int64_t c0, int64_t M, int64_t N, int lane) {
     constexpr int CW = ROW / sizeof(T), VEC = Vec16<T>::VEC;
     auto at = [&](int r, int j) { return out + r * ROW + ((j ^ (r & 7)) << 4); };
+    // vector accesses: lane's chunk lane % 8 of rows lane / 8 + 4 p, p < 8
+    const int64_t mine = (r0 + (lane >> 3)) * N + c0 + VEC * (lane & 7);
+    const int rows = c0 + VEC * (lane & 7) < N ? (M - r0 < 32 ? (int)(M - r0) : 32) - (lane >> 3) : 0;
     auto put = [&](T* dst) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at(lane, j)) = Vec16<T>::pack(v + VEC * j);
         __syncwarp();
         if (ep.vec) {
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const int r = 4 * p + (lane >> 3), j = lane & 7;
-                if (r0 + r < M && c0 + VEC * j < N)
-                    st_v4(dst + (r0 + r) * N + c0 + VEC * j, *reinterpret_cast<const uint4*>(at(r, j)));
-            }
+            for (int p = 0; p < 8; ++p)
+                if (4 * p < rows)
+                    st_v4(dst + mine + p * 4 * N, *reinterpret_cast<const uint4*>(at(4 * p + (lane >> 3), lane & 7)));
         } else {
 #pragma unroll 2
             for (int r = 0; r < 32 && r0 + r < M; ++r)
@@ -230,18 +241,25 @@ __device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[R
         __syncwarp();
     };
     if (ep.bias) {
+        if (c0 + CW <= N && (uintptr_t)ep.bias % 16 == 0) {
 #pragma unroll
-        for (int j = 0; j < CW; ++j) v[j] += c0 + j < N ? __ldg(ep.bias + c0 + j) : 0.f;
+            for (int j = 0; j < CW; j += 4) {
+                const float4 b = __ldg(reinterpret_cast<const float4*>(ep.bias + c0 + j));
+                v[j] += b.x; v[j + 1] += b.y; v[j + 2] += b.z; v[j + 3] += b.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < CW; ++j) v[j] += c0 + j < N ? __ldg(ep.bias + c0 + j) : 0.f;
+        }
     }
     if (ep.z) put(ep.z);
     if (ep.residual) {
         if (ep.vec) {
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const int r = 4 * p + (lane >> 3), j = lane & 7;
-                if (r0 + r < M && c0 + VEC * j < N)
-                    *reinterpret_cast<uint4*>(at(r, j)) = ld_stream_v4(ep.residual + (r0 + r) * N + c0 + VEC * j);
-            }
+            for (int p = 0; p < 8; ++p)
+                if (4 * p < rows)
+                    *reinterpret_cast<uint4*>(at(4 * p + (lane >> 3), lane & 7)) =
+                        ld_stream_v4(ep.residual + mine + p * 4 * N);
         } else {
 #pragma unroll 2
             for (int r = 0; r < 32 && r0 + r < M; ++r)
@@ -439,6 +457,7 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
             int m, n;
             tile_at(i, mt, nt, m, n);
             const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q;
+            prefetch_residual(ep, r0, (int64_t)n * BN + h * (BN / 2), BN / 2, M, N, lane);
             if (!wait.warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC)) break;
             tc_fence_after();
 #pragma unroll 1
@@ -623,6 +642,7 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
             int m, n;
             tile_at(i, mt, nt, m, n);
             const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q, c0 = (int64_t)n * BN + h * (BN / 2);
+            prefetch_residual(ep, r0, c0, BN / 2, M, N, lane);
             float sum[2][32] = {};
             for (int kb = 0; kb < kblocks; kb += C::CHUNK, ++tc) {
                 const int buf = tc & 1;
