@@ -10,8 +10,8 @@
 //     forms 256 x BN tiles with cta_group::2 MMAs (M = 256): each CTA loads its 128 rows of A and
 //     half of B's rows, so a byte of shared memory feeds twice the MMA work of a single CTA's tile.
 //     Persistent: the accumulators are double buffered in TMEM, and the epilogue of one tile runs
-//     under the MMAs of the next.  Warp roles (320 threads): 0 TMA, 1 MMA issue (first CTA of the
-//     pair), 2-9 epilogue.
+//     under the MMAs of the next.  Warp roles: 0 TMA, 1 MMA issue (first CTA of the pair), 2-17
+//     epilogue.
 //   * gemm_split_kernel, for the others (single tokens, small or thin products).  The side with
 //     contiguous output goes on the 128 MMA rows, so a few tokens are a narrow MMA N and a warp's
 //     stores are contiguous.  A cluster of S CTAs shares a tile by splitting K; the partial tiles
@@ -45,8 +45,13 @@ using bf16 = __nv_bfloat16;
 constexpr int BK = 64;                  // K of a block: one 128-byte row
 constexpr int ROW = 128;                // bytes
 constexpr int BLK = 64 * ROW;           // a 64 x 64 box of an operand whose M / N index is contiguous
-constexpr int THREADS = 320;
-constexpr int EPI = 8;                  // epilogue warps: two per TMEM lane quarter
+constexpr int EPI = 8;                  // epilogue warps of the split kernel: two per TMEM lane quarter
+constexpr int THREADS = 32 * (2 + EPI);
+// The pair kernels have four per lane quarter: an activation's chains of dependent operations need
+// more warps than that to cover (T = 4096, 1024 -> 4096 with GELU, 8 warps: 56 us, 28 of them without it)
+constexpr int PAIR_EPI = 16;
+constexpr int CW = 32;                  // columns of outputs that a warp of theirs forms at a time
+constexpr int PAIR_THREADS = 32 * (2 + PAIR_EPI);
 constexpr unsigned long long kWaitNs = 1000000000ull;    // 1 s per wait
 constexpr unsigned long long kDrainNs = 2000000000ull;   // 2 s for the drains at exit
 constexpr unsigned long long kLandNs = 2000000ull;       // after a failed wait: loads in flight land
@@ -205,38 +210,37 @@ template <typename T>
 __device__ __forceinline__ void prefetch_residual(const Epilogue<T>& ep, int64_t r0, int64_t c0, int cols, int64_t M,
                                                   int64_t N, int lane) {
     if (!ep.residual || r0 + lane >= M) return;
-    for (int c = 0; c < cols && c0 + c < N; c += ROW / (int)sizeof(T))
+    for (int c = 0; c < cols && c0 + c < N; c += CW)
         asm volatile("prefetch.global.L2 [%0];" :: "l"(ep.residual + (r0 + lane) * N + c0 + c));
 }
 
-// The outputs of a warp's 32 rows x 128 bytes of columns at (r0, c0) from their sums, a row per lane:
-// v = act(v + bias) + residual, and z.  Between registers and memory (128 bytes of a row per eight
-// lanes) the block goes through the warp's 4 KB of shared memory, swizzled by 16-byte chunks.
+// The outputs of a warp's 32 rows x CW columns at (r0, c0) from their sums, a row per lane:
+// v = act(v + bias) + residual, and z.  Between registers and memory (whole rows of the block by
+// neighbouring lanes) the block goes through the warp's shared memory, swizzled by 16-byte chunks.
 template <typename T>
-__device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[ROW / sizeof(T)], unsigned char* out,
-                                             int64_t r0, int64_t c0, int64_t M, int64_t N, int lane) {
-    constexpr int CW = ROW / sizeof(T), VEC = Vec16<T>::VEC;
-    auto at = [&](int r, int j) { return out + r * ROW + ((j ^ (r & 7)) << 4); };
-    // vector accesses: lane's chunk lane % 8 of rows lane / 8 + 4 p, p < 8
-    const int64_t mine = (r0 + (lane >> 3)) * N + c0 + VEC * (lane & 7);
-    const int rows = c0 + VEC * (lane & 7) < N ? (M - r0 < 32 ? (int)(M - r0) : 32) - (lane >> 3) : 0;
+__device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[CW], unsigned char* out, int64_t r0,
+                                             int64_t c0, int64_t M, int64_t N, int lane) {
+    constexpr int VEC = Vec16<T>::VEC, CPR = CW / VEC;          // 16-byte chunks per row: 4 or 8
+    auto at = [&](int r, int j) { return out + (r * CPR + (j ^ (CPR == 8 ? r & 7 : (r >> 1) & 3))) * 16; };
+    // vector accesses: lane's chunk lane % CPR of rows lane / CPR + (32 / CPR) p, p < CPR
+    constexpr int STEP = 32 / CPR;
+    const int lr = lane / CPR, lc = lane % CPR;
+    const int64_t mine = (r0 + lr) * N + c0 + VEC * lc;
+    const int rows = c0 + VEC * lc < N ? (M - r0 < 32 ? (int)(M - r0) : 32) - lr : 0;
     auto put = [&](T* dst) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(at(lane, j)) = Vec16<T>::pack(v + VEC * j);
+        for (int j = 0; j < CPR; ++j) *reinterpret_cast<uint4*>(at(lane, j)) = Vec16<T>::pack(v + VEC * j);
         __syncwarp();
         if (ep.vec) {
 #pragma unroll
-            for (int p = 0; p < 8; ++p)
-                if (4 * p < rows)
-                    st_v4(dst + mine + p * 4 * N, *reinterpret_cast<const uint4*>(at(4 * p + (lane >> 3), lane & 7)));
+            for (int p = 0; p < CPR; ++p)
+                if (STEP * p < rows)
+                    st_v4(dst + mine + p * STEP * N, *reinterpret_cast<const uint4*>(at(STEP * p + lr, lc)));
         } else {
 #pragma unroll 2
             for (int r = 0; r < 32 && r0 + r < M; ++r)
-#pragma unroll
-                for (int u = 0; u < CW / 32; ++u) {
-                    const int c = lane + 32 * u;
-                    if (c0 + c < N) dst[(r0 + r) * N + c0 + c] = reinterpret_cast<const T*>(at(r, c / VEC))[c % VEC];
-                }
+                if (c0 + lane < N)
+                    dst[(r0 + r) * N + c0 + lane] = reinterpret_cast<const T*>(at(r, lane / VEC))[lane % VEC];
         }
         __syncwarp();
     };
@@ -256,18 +260,14 @@ __device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[R
     if (ep.residual) {
         if (ep.vec) {
 #pragma unroll
-            for (int p = 0; p < 8; ++p)
-                if (4 * p < rows)
-                    *reinterpret_cast<uint4*>(at(4 * p + (lane >> 3), lane & 7)) =
-                        ld_stream_v4(ep.residual + mine + p * 4 * N);
+            for (int p = 0; p < CPR; ++p)
+                if (STEP * p < rows)
+                    *reinterpret_cast<uint4*>(at(STEP * p + lr, lc)) = ld_stream_v4(ep.residual + mine + p * STEP * N);
         } else {
 #pragma unroll 2
             for (int r = 0; r < 32 && r0 + r < M; ++r)
-#pragma unroll
-                for (int u = 0; u < CW / 32; ++u) {
-                    const int c = lane + 32 * u;
-                    if (c0 + c < N) reinterpret_cast<T*>(at(r, c / VEC))[c % VEC] = ep.residual[(r0 + r) * N + c0 + c];
-                }
+                if (c0 + lane < N)
+                    reinterpret_cast<T*>(at(r, lane / VEC))[lane % VEC] = ep.residual[(r0 + r) * N + c0 + lane];
         }
         __syncwarp();
     }
@@ -277,7 +277,7 @@ __device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[R
     });
     if (ep.residual) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < CPR; ++j) {
             float f[VEC];
             Vec16<T>::unpack(*reinterpret_cast<uint4*>(at(lane, j)), f);
 #pragma unroll
@@ -298,11 +298,12 @@ struct PairCfg {
     static constexpr int KS = BN == 256 ? 1 : 2;
     static constexpr int STAGE = KS * BLOCK;
     static constexpr int NS = 196608 / STAGE;                  // 6 stages at BN = 256, 4 at BN = 128
-    static constexpr int OUT = EPI * 32 * ROW;                 // a 32 x 64 bf16 block per epilogue warp
+    static constexpr int OUT = PAIR_EPI * 32 * CW * 2;         // a block of outputs per epilogue warp
     static constexpr int SMEM = NS * STAGE + OUT + 1024;       // + alignment slack
     static constexpr int TMEM_COLS = 512;                      // all of it, so both CTAs hold column 0
     static_assert(SMEM <= 232448 - 512, "shared memory");
     static_assert(2 * BN <= TMEM_COLS, "two accumulators");
+    static_assert(BN / 4 % CW == 0, "whole blocks per epilogue warp");
 };
 
 // Tiles in an order that keeps the operands of those in flight in L2: bands of 8 tile rows, each
@@ -318,7 +319,7 @@ __device__ __forceinline__ void tile_at(int64_t i, int mt, int nt, int& m, int& 
 }
 
 template <int BN, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<bf16> ep, int64_t M, int64_t N, int kblocks, int mt,
                  int nt, Limits lim) {
     using C = PairCfg<BN>;
@@ -345,7 +346,7 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf(b), 1);
-            mbar_init(acce(b), 2 * EPI);
+            mbar_init(acce(b), 2 * PAIR_EPI);
         }
         mbar_init(drained, 1);
         abort_flag = 0;
@@ -447,31 +448,30 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
         }
         __syncwarp();
     } else {
+        // a warp has BN / 4 columns of its lane quarter
         const int q = warp & 3, h = (warp - 2) >> 2;
-        const uint32_t tq = tm + ((uint32_t)(32 * q) << 16);
-        unsigned char* out = sm + NS * C::STAGE + (warp - 2) * 32 * ROW;
+        const uint32_t tq = tm + ((uint32_t)(32 * q) << 16) + h * (BN / 4);
+        unsigned char* out = sm + NS * C::STAGE + (warp - 2) * 32 * CW * 2;
         const uint32_t acce_first[2] = {mapa(acce(0), 0), mapa(acce(1), 0)};
         int tc = 0;
         for (int64_t i = first; i < tiles; i += stride, ++tc) {
             const int buf = tc & 1;
             int m, n;
             tile_at(i, mt, nt, m, n);
-            const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q;
-            prefetch_residual(ep, r0, (int64_t)n * BN + h * (BN / 2), BN / 2, M, N, lane);
+            const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q, c0 = (int64_t)n * BN + h * (BN / 4);
+            prefetch_residual(ep, r0, c0, BN / 4, M, N, lane);
             if (!wait.warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < BN / 2; cc += 64) {
-                const int64_t c0 = (int64_t)n * BN + h * (BN / 2) + cc;
-                if (c0 >= N || r0 >= M) continue;
-                float v[64];
-                tmem_ld32(tq + buf * BN + h * (BN / 2) + cc, reinterpret_cast<float(&)[32]>(v[0]));
-                tmem_ld32(tq + buf * BN + h * (BN / 2) + cc + 32, reinterpret_cast<float(&)[32]>(v[32]));
-                finish_block<bf16>(ep, v, out, r0, c0, M, N, lane);
+            for (int c = 0; c < BN / 4; c += CW) {
+                if (c0 + c >= N || r0 >= M) continue;
+                float v[CW];
+                tmem_ld32(tq + buf * BN + c, v);
+                finish_block<bf16>(ep, v, out, r0, c0 + c, M, N, lane);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(acce_first[buf]);
+            if (lane == 0) arrive_cluster(buf ? acce_first[1] : acce_first[0]);
         }
     }
     tc_fence_before();
@@ -498,17 +498,18 @@ struct F32Cfg {
     static constexpr int A_PLANE = 128 * ROW, B_PLANE = BN / 2 * ROW;      // one of the three parts
     static constexpr int STAGE = 3 * (A_PLANE + B_PLANE);                  // 64 of K
     static constexpr int NS = 2;
-    static constexpr int OUT = EPI * 32 * ROW;
+    static constexpr int OUT = PAIR_EPI * 32 * CW * 4;
     static constexpr int SMEM = NS * STAGE + OUT + 1024;
     static constexpr int TMEM_COLS = 512;
     static constexpr int CHUNK = 4;
     static_assert(SMEM <= 232448 - 512, "shared memory");
+    static_assert(BN == 4 * CW, "a block per epilogue warp");
 };
 
 // The maps cover the planes as a third dimension and bring the three parts of a box together: rows
 // along K as [part][row], others as [64 rows][part][64 of K].
 template <bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<float> ep, int64_t M, int64_t N,
                 int kblocks, int mt, int nt, Limits lim) {
     using C = F32Cfg;
@@ -535,7 +536,7 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf(b), 1);
-            mbar_init(acce(b), 2 * EPI);
+            mbar_init(acce(b), 2 * PAIR_EPI);
         }
         mbar_init(drained, 1);
         abort_flag = 0;
@@ -633,37 +634,32 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
         __syncwarp();
     } else {
         const int q = warp & 3, h = (warp - 2) >> 2;
-        const uint32_t tq = tm + ((uint32_t)(32 * q) << 16) + h * (BN / 2);
-        unsigned char* out = sm + NS * C::STAGE + (warp - 2) * 32 * ROW;
+        const uint32_t tq = tm + ((uint32_t)(32 * q) << 16) + h * CW;
+        unsigned char* out = sm + NS * C::STAGE + (warp - 2) * 32 * CW * 4;
         const uint32_t acce_first[2] = {mapa(acce(0), 0), mapa(acce(1), 0)};
         int tc = 0;
         bool ok = true;
         for (int64_t i = first; ok && i < tiles; i += stride) {
             int m, n;
             tile_at(i, mt, nt, m, n);
-            const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q, c0 = (int64_t)n * BN + h * (BN / 2);
-            prefetch_residual(ep, r0, c0, BN / 2, M, N, lane);
-            float sum[2][32] = {};
+            const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q, c0 = (int64_t)n * BN + h * CW;
+            prefetch_residual(ep, r0, c0, CW, M, N, lane);
+            float sum[CW] = {};
             for (int kb = 0; kb < kblocks; kb += C::CHUNK, ++tc) {
                 const int buf = tc & 1;
                 if (!(ok = wait.warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC))) break;
                 tc_fence_after();
+                float v[CW], w[CW];
+                tmem_ld32(tq + buf * 2 * BN, v);
+                tmem_ld32(tq + buf * 2 * BN + BN, w);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float v[32], w[32];
-                    tmem_ld32(tq + buf * 2 * BN + 32 * u, v);
-                    tmem_ld32(tq + buf * 2 * BN + BN + 32 * u, w);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) sum[u][j] += v[j] + w[j];
-                }
+                for (int j = 0; j < CW; ++j) sum[j] += v[j] + w[j];
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(buf ? acce_first[1] : acce_first[0]);
             }
             if (!ok) break;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                if (c0 + 32 * u < N && r0 < M) finish_block<float>(ep, sum[u], out, r0, c0 + 32 * u, M, N, lane);
+            if (c0 < N && r0 < M) finish_block<float>(ep, sum, out, r0, c0, M, N, lane);
         }
     }
     tc_fence_before();
@@ -972,7 +968,7 @@ cudaError_t pair_launch(const GemmArgs& g, int sms) {
     const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + BN - 1) / BN);
     const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_pdl(kern, dim3(grid), dim3(THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<bf16>(g), g.M, g.N,
+    return launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<bf16>(g), g.M, g.N,
                       (int)((g.K + BK - 1) / BK), mt, nt, limits());
 }
 
@@ -995,7 +991,7 @@ cudaError_t f32_launch(const GemmArgs& g, const F32Planes& f, int sms) {
     const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + C::BN - 1) / C::BN);
     const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_pdl(kern, dim3(grid), dim3(THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<float>(g), g.M, g.N,
+    return launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<float>(g), g.M, g.N,
                       (int)((g.K + BK - 1) / BK), mt, nt, limits());
 }
 
