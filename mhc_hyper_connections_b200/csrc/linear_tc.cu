@@ -184,8 +184,15 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&f)[8]) {
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                 :: "l"(map), "r"(c0), "r"(c1), "r"(src) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// operands, and the outputs D and z of a pair kernel (where their rows are 16-byte aligned)
 struct Maps {
-    CUtensorMap a, b;
+    CUtensorMap a, b, d, z;
 };
 
 // The wait limit, and the failure-path test hook: stages after which a CTA stops loading (< 0: never)
@@ -215,33 +222,39 @@ __device__ __forceinline__ void prefetch_residual(const Epilogue<T>& ep, int64_t
 }
 
 // The outputs of a warp's 32 rows x CW columns at (r0, c0) from their sums, a row per lane:
-// v = act(v + bias) + residual, and z.  Between registers and memory (whole rows of the block by
-// neighbouring lanes) the block goes through the warp's shared memory, swizzled by 16-byte chunks.
+// v = act(v + bias) + residual, and z.  Between registers and memory the block goes through the warp's
+// shared memory, swizzled by 16-byte chunks as TMA stores of 64- and 128-byte rows expect them: written
+// by the lanes instead, dW of T = 64, 4096 -> 16384 (134 MB out) took 50 us, 21 of them in the stores.
+// lane 0 has the stores in flight; whoever ends the kernel waits for them.
 template <typename T>
-__device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[CW], unsigned char* out, int64_t r0,
-                                             int64_t c0, int64_t M, int64_t N, int lane) {
+__device__ __forceinline__ void finish_block(const Epilogue<T>& ep, const Maps& maps, float (&v)[CW],
+                                             unsigned char* out, int64_t r0, int64_t c0, int64_t M, int64_t N,
+                                             int lane) {
     constexpr int VEC = Vec16<T>::VEC, CPR = CW / VEC;          // 16-byte chunks per row: 4 or 8
     auto at = [&](int r, int j) { return out + (r * CPR + (j ^ (CPR == 8 ? r & 7 : (r >> 1) & 3))) * 16; };
-    // vector accesses: lane's chunk lane % CPR of rows lane / CPR + (32 / CPR) p, p < CPR
+    // vector loads: lane's chunk lane % CPR of rows lane / CPR + (32 / CPR) p, p < CPR
     constexpr int STEP = 32 / CPR;
     const int lr = lane / CPR, lc = lane % CPR;
     const int64_t mine = (r0 + lr) * N + c0 + VEC * lc;
     const int rows = c0 + VEC * lc < N ? (M - r0 < 32 ? (int)(M - r0) : 32) - lr : 0;
-    auto put = [&](T* dst) {
+    auto free_block = [&] {              // the last store has read it
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+    };
+    auto put = [&](T* dst, const CUtensorMap& map) {
 #pragma unroll
         for (int j = 0; j < CPR; ++j) *reinterpret_cast<uint4*>(at(lane, j)) = Vec16<T>::pack(v + VEC * j);
-        __syncwarp();
         if (ep.vec) {
-#pragma unroll
-            for (int p = 0; p < CPR; ++p)
-                if (STEP * p < rows)
-                    st_v4(dst + mine + p * STEP * N, *reinterpret_cast<const uint4*>(at(STEP * p + lr, lc)));
-        } else {
-#pragma unroll 2
-            for (int r = 0; r < 32 && r0 + r < M; ++r)
-                if (c0 + lane < N)
-                    dst[(r0 + r) * N + c0 + lane] = reinterpret_cast<const T*>(at(r, lane / VEC))[lane % VEC];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tma_store_2d(&map, smem_u32(out), (int)c0, (int)r0);
+            return;
         }
+        __syncwarp();
+#pragma unroll 2
+        for (int r = 0; r < 32 && r0 + r < M; ++r)
+            if (c0 + lane < N)
+                dst[(r0 + r) * N + c0 + lane] = reinterpret_cast<const T*>(at(r, lane / VEC))[lane % VEC];
         __syncwarp();
     };
     if (ep.bias) {
@@ -256,8 +269,10 @@ __device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[C
             for (int j = 0; j < CW; ++j) v[j] += c0 + j < N ? __ldg(ep.bias + c0 + j) : 0.f;
         }
     }
-    if (ep.z) put(ep.z);
+    free_block();
+    if (ep.z) put(ep.z, maps.z);
     if (ep.residual) {
+        if (ep.z) free_block();
         if (ep.vec) {
 #pragma unroll
             for (int p = 0; p < CPR; ++p)
@@ -284,7 +299,8 @@ __device__ __forceinline__ void finish_block(const Epilogue<T>& ep, float (&v)[C
             for (int e = 0; e < VEC; ++e) v[VEC * j + e] += f[e];
         }
     }
-    put(ep.D);                           // a lane overwrites its own row of the residual
+    if (ep.z && !ep.residual) free_block();
+    put(ep.D, maps.d);                   // a lane overwrites its own row of the residual
 }
 
 // ------------------------------------------------------------------------- the pair kernel
@@ -467,12 +483,14 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
                 if (c0 + c >= N || r0 >= M) continue;
                 float v[CW];
                 tmem_ld32(tq + buf * BN + c, v);
-                finish_block<bf16>(ep, v, out, r0, c0 + c, M, N, lane);
+                finish_block<bf16>(ep, maps, v, out, r0, c0 + c, M, N, lane);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(buf ? acce_first[1] : acce_first[0]);
         }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -659,8 +677,10 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
                 if (lane == 0) arrive_cluster(buf ? acce_first[1] : acce_first[0]);
             }
             if (!ok) break;
-            if (c0 < N && r0 < M) finish_block<float>(ep, sum, out, r0, c0, M, N, lane);
+            if (c0 < N && r0 < M) finish_block<float>(ep, maps, sum, out, r0, c0, M, N, lane);
         }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -919,6 +939,27 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t K, int64_t 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// An output of M rows of N elements, stored in blocks of 32 x CW
+template <typename T>
+bool make_map_out(CUtensorMap* map, void* p, int64_t M, int64_t N) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    const cuuint64_t str[1] = {(cuuint64_t)N * sizeof(T)};
+    const cuuint32_t box[2] = {CW, 32};
+    const cuuint32_t e1[2] = {1, 1};
+    return enc(map, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p, dims, str,
+               box, e1, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               sizeof(T) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The maps of a pair kernel's outputs, where it stores through them
+template <typename T>
+bool output_maps(Maps* maps, const Epilogue<T>& ep, int64_t M, int64_t N) {
+    return !ep.vec || (make_map_out<T>(&maps->d, ep.D, M, N) && (!ep.z || make_map_out<T>(&maps->z, ep.z, M, N)));
+}
+
 // The three planes of an fp32 operand, `plane` elements apart: boxes of 64 x (box_rows or 64) x 3
 bool make_map_planes(CUtensorMap* map, const void* p, int64_t rows, int64_t K, int64_t ld, int64_t plane, bool mn,
                      int box_rows) {
@@ -962,13 +1003,15 @@ cudaError_t pair_launch(const GemmArgs& g, int sms) {
     auto kern = gemm_pair_kernel<BN, A_MN, B_MN>;
     cudaError_t e = allow_smem(kern, C::SMEM);
     if (e != cudaSuccess) return e;
-    Maps maps;
-    if (!make_map(&maps.a, g.A, g.M, g.K, g.lda, A_MN, 128) || !make_map(&maps.b, g.B, g.N, g.K, g.ldb, B_MN, BN / 2))
+    Maps maps{};
+    const Epilogue<bf16> ep = epilogue_of<bf16>(g);
+    if (!make_map(&maps.a, g.A, g.M, g.K, g.lda, A_MN, 128) || !make_map(&maps.b, g.B, g.N, g.K, g.ldb, B_MN, BN / 2) ||
+        !output_maps(&maps, ep, g.M, g.N))
         return cudaErrorInvalidValue;
     const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + BN - 1) / BN);
     const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<bf16>(g), g.M, g.N,
+    return launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)C::SMEM, g.stream, maps, ep, g.M, g.N,
                       (int)((g.K + BK - 1) / BK), mt, nt, limits());
 }
 
@@ -984,14 +1027,16 @@ cudaError_t f32_launch(const GemmArgs& g, const F32Planes& f, int sms) {
     auto kern = gemm_f32_kernel<A_MN, B_MN>;
     cudaError_t e = allow_smem(kern, C::SMEM);
     if (e != cudaSuccess) return e;
-    Maps maps;
+    Maps maps{};
+    const Epilogue<float> ep = epilogue_of<float>(g);
     if (!make_map_planes(&maps.a, f.A, g.M, g.K, f.lda, f.a_plane, A_MN, 128) ||
-        !make_map_planes(&maps.b, f.B, g.N, g.K, f.ldb, f.b_plane, B_MN, C::BN / 2))
+        !make_map_planes(&maps.b, f.B, g.N, g.K, f.ldb, f.b_plane, B_MN, C::BN / 2) ||
+        !output_maps(&maps, ep, g.M, g.N))
         return cudaErrorInvalidValue;
     const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + C::BN - 1) / C::BN);
     const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)C::SMEM, g.stream, maps, epilogue_of<float>(g), g.M, g.N,
+    return launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)C::SMEM, g.stream, maps, ep, g.M, g.N,
                       (int)((g.K + BK - 1) / BK), mt, nt, limits());
 }
 
@@ -1001,7 +1046,7 @@ cudaError_t split_launch(const GemmArgs& g, int S) {
     auto kern = gemm_split_kernel<BN, A_MN, B_MN>;
     cudaError_t e = allow_smem(kern, C::SMEM);
     if (e != cudaSuccess) return e;
-    Maps maps;                           // the product's B side on the MMA rows
+    Maps maps{};                         // the product's B side on the MMA rows
     if (!make_map(&maps.a, g.B, g.N, g.K, g.ldb, A_MN, 128) || !make_map(&maps.b, g.A, g.M, g.K, g.lda, B_MN, BN))
         return cudaErrorInvalidValue;
     const int mt = (int)((g.N + 127) / 128);
