@@ -323,7 +323,7 @@ mhc_status mhc_layer_norm(const void* x, const float* weight, const float* bias,
                           mhc_stream_t stream);
 
 /*
- * mhc_layer_norm_backward_workspace_bytes -- device workspace mhc_layer_norm_backward needs
+ * mhc_layer_norm_backward_workspace_bytes -- device workspace mhc_layer_norm_backward takes
  * for (T, d); 0 for a shape it rejects and for T == 0.  Host-side, launches nothing.
  */
 size_t mhc_layer_norm_backward_workspace_bytes(int64_t T, int d);

@@ -168,6 +168,7 @@ struct LnArgs {
     void* dx;                    // null: not wanted
     float* dw;                   // null: not wanted
     float* db;
+    bool late;                   // set by the backward launch: the row kernel waits at its end
     float* part;                 // layer_norm_part_floats floats; null when neither dw nor db is wanted
     cudaStream_t stream;
 };

@@ -11,18 +11,20 @@
 // output; sums are fp32, and the variance is summed around the mean (a second walk over the
 // registers), which a mean far from zero does not spoil.
 //
-// A row belongs to one warp (WARP, rows of up to 4 vectors per lane) or to one thread block.  A
-// thread owns the same NV vectors of VEC columns in every row it sees, so w and b are loaded once
-// and the backward's column sums stay in registers until the thread's last row.
-//   * ring kernels, for aligned rows and more of them than SMs: a warp of its own brings the next rows
-//     into a ring in shared memory by bulk copies, so the loads in flight do not depend on what the
-//     other warps are doing (without it a block's reductions and stores left HBM idle: 86 us forward at
-//     T = 16384, d = 4096, bf16);
-//   * register kernels, for few rows (latency counts: one vector per thread, no ring to set up) and
-//     for rows that are not 16-byte aligned (one element at a time);
+// A row belongs to 8, 16 or 32 lanes or to a thread block.  A thread owns the same NV vectors of VEC
+// columns in every row it sees, so w and b are loaded once and the backward's column sums stay in
+// registers until the thread's last row.
+//   * ring kernels, for aligned rows and more of them than SMs: bulk copies bring the next rows into a
+//     ring in shared memory, so the loads in flight do not depend on what the warps are doing (without it
+//     a block's reductions and stores left HBM idle: 86 us forward at T = 16384, d = 4096, bf16).  One
+//     ring and a warp that fills it per block, or (forward, long rows) one per warp: 49 us, 5.5 TB/s.
+//   * shift kernels, the same for rows that are not a multiple of 16 bytes;
+//   * register kernels, for few rows (latency counts: one vector per thread, no ring to set up), and one
+//     element at a time for unaligned rows that the shift kernels do not take;
 //   * long kernels, for rows beyond the registers of a block: three walks over the row.
 // Column sums are added up in a fixed order: over a group's rows, over a block's warps in shared
-// memory, and over the blocks by a second kernel that reads one fp32 row pair per block.
+// memory, and over the blocks by a second kernel that reads one fp32 row pair per block; or, for few
+// rows, by a kernel that reads the rows once more beside the first one.
 #include <atomic>
 
 #include "common.cuh"
@@ -39,6 +41,10 @@ namespace {
 // blocks that write column-sum rows for the second kernel: two per SM of a 148-SM device, and up to
 // eight where rows are short (T = 16384, d = 1024, bf16: 39 us with two)
 int bwd_blocks(int d) { return d >= 4096 ? 296 : d <= 1024 ? 1184 : 296 * 4096 / d; }
+// Up to here the column sums come straight from the rows, read a second time from L2 while the row
+// kernel runs; above it from the row kernel's registers through `part`.  d = 2560, bf16, T = 128: 3.5 us
+// against 8.2, T = 500: 6.4 against 9.6, T = 1000: 14.4 against 11.5.
+constexpr int FEW_ROWS = 512;
 constexpr int WARPS = 8;               // warps per block where a row belongs to a warp
 
 // VEC elements as they lie in memory: 16 bytes, or one element where rows are not 16-byte aligned
@@ -88,6 +94,20 @@ __device__ __forceinline__ void group_sum(float (&v)[R], float* buf, int& phase,
 
 // threads of a block: a warp per row uses WARPS warps; a block per row as many threads as the row
 // needs, up to 1024 with one vector each (few rows) and 512 with more, which the registers allow
+// The wait for the kernels before this one: ahead of its reads, or (late) at its end, for a kernel
+// launched behind one that reads the same inputs, that waited for them itself before it let this one
+// start, and whose outputs this one does not touch.  Waiting at the end keeps the stream's order for what
+// follows.
+struct StreamOrder {
+    bool late;
+    __device__ __forceinline__ explicit StreamOrder(bool l) : late(l) {
+        if (!late) pdl_wait();
+    }
+    __device__ __forceinline__ ~StreamOrder() {
+        if (late) pdl_wait();
+    }
+};
+
 template <int NV, bool WARP> constexpr int MAX_THREADS = WARP ? 32 * WARPS : (NV == 1 ? 1024 : 512);
 
 template <typename T, int VEC, int NV, int R, bool WARP>
@@ -219,13 +239,13 @@ template <typename T, int VEC, int NV, int R, bool WARP>
 __global__ void __launch_bounds__(MAX_THREADS<NV, WARP>)
 ln_bwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
                               const float* __restrict__ rstd, const T* __restrict__ dy, int64_t Tn, int d,
-                              T* __restrict__ dx, float* __restrict__ part) {
+                              T* __restrict__ dx, float* __restrict__ part, bool late) {
     using P = Pack<T, VEC>;
     __shared__ float buf[WARP ? 1 : 64 * 2 * R];
     extern __shared__ float cols[];        // WARP: [2][d] column sums of the block
     int phase = 0;
     pdl_launch_next();
-    pdl_wait();
+    const StreamOrder order(late);
     const int nthr = WARP ? 32 : blockDim.x;
     const int idx = WARP ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t groups = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
@@ -343,11 +363,12 @@ template <typename T>
 __global__ void __launch_bounds__(1024)
 ln_bwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
                                    const float* __restrict__ mean, const float* __restrict__ rstd,
-                                   const T* __restrict__ dy, int64_t Tn, int d, T* __restrict__ dx, float* part) {
+                                   const T* __restrict__ dy, int64_t Tn, int d, T* __restrict__ dx, float* part,
+                                   bool late) {
     __shared__ float buf[64 * 2];
     int phase = 0;
     pdl_launch_next();
-    pdl_wait();
+    const StreamOrder order(late);
     const float inv_d = 1.0f / (float)d;
     float* pw = part ? part + (int64_t)blockIdx.x * 2 * d : nullptr;
     for (int64_t row = blockIdx.x; row < Tn; row += gridDim.x) {
@@ -732,7 +753,7 @@ template <typename T, int NV, int R, int G, int TH>
 __global__ void __launch_bounds__(TH + 32, 1)
 ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
                    const float* __restrict__ rstd, const T* __restrict__ dy, int64_t Tn, int d, T* __restrict__ dx,
-                   float* __restrict__ part, int slots, Limits lim) {
+                   float* __restrict__ part, bool late, int slots, Limits lim) {
     constexpr int VEC = Vec16<T>::VEC, HV = VEC / 2;
     constexpr int GROUPS = G ? WARPS * (32 / (G ? G : 32)) : 1, B = GROUPS * R;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -744,7 +765,7 @@ ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
     if (threadIdx.x == 0) ring_init(bars, &abort_flag, slots, consumers >> 5);
     __syncthreads();
     pdl_launch_next();
-    pdl_wait();
+    const StreamOrder order(late);
     Ring ring{bars, &abort_flag, slots, lim};
     const int64_t batches = (Tn + B - 1) / B, row_bytes = (int64_t)d * sizeof(T);
     if (warp == consumers >> 5) {
@@ -883,21 +904,405 @@ ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
     }
 }
 
-// out[c] = sum over the P blocks of part[p][c], c < 2 d: a block takes 32 columns, its 16 warps a
+// ---- rows that are not 16-byte aligned
+//
+// A row of d elements that is not a multiple of 16 bytes starts anywhere within a 16-byte word, but rows
+// eight apart start at the same place in theirs.  So a block takes every (8 k)-th row, and sees one
+// shift s: its word j holds the columns VEC j - s .. VEC j - s + VEC - 1 of each of them, and the kernels
+// are those of aligned rows but for the two words at the ends, which hold elements of other rows too.
+// The bulk copies bring the whole words around a row; the last row's copy ends with the last whole word
+// of the array.  Arrays themselves are 16-byte aligned.
+template <typename T>
+struct Shifted {
+    static constexpr int VEC = Vec16<T>::VEC;
+    const T* p;
+    int64_t Tn;
+    int d, s, row_bytes, slot_bytes;     // slot_bytes: room for a row's words
+
+    __device__ __forceinline__ Shifted(const T* p_, int64_t Tn_, int d_, int64_t row)
+        : p(p_), Tn(Tn_), d(d_), s((int)(row * d_ * (int64_t)sizeof(T) & 15) / (int)sizeof(T)),
+          row_bytes(d_ * (int)sizeof(T)), slot_bytes((row_bytes + 15) / 16 * 16 + 16) {}
+    // first byte of the row's words, and how many bytes of them are copied
+    __device__ __forceinline__ int64_t at(int64_t row) const { return row * row_bytes & ~(int64_t)15; }
+    __device__ __forceinline__ int bytes(int64_t row) const {
+        const int64_t up = (row * row_bytes + row_bytes + 15) & ~(int64_t)15, last = Tn * row_bytes & ~(int64_t)15;
+        return (int)((up < last ? up : last) - at(row));
+    }
+    __device__ __forceinline__ void load(int64_t row, uint32_t dst, uint32_t bar) const {
+        ptx::bulk_g2s(dst, reinterpret_cast<const unsigned char*>(p) + at(row), bytes(row), bar);
+    }
+    // words of a row, and how many elements of the first and the last belong to other rows
+    __device__ __forceinline__ int words() const { return (d + s + VEC - 1) / VEC; }
+    __device__ __forceinline__ int spare() const { return words() * VEC - d - s; }
+    // ones over the elements of word j that belong to the row
+    __device__ __forceinline__ uint4 mask(int j) const {
+        uint32_t m[4] = {};
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = j * VEC + i - s;
+            if (c >= 0 && c < d) m[i * 4 / VEC] |= sizeof(T) == 4 ? 0xFFFFFFFFu : 0xFFFFu << (16 * (i & 1));
+        }
+        return make_uint4(m[0], m[1], m[2], m[3]);
+    }
+    // The last row may end inside a word that is not copied: its elements from memory, into the slot, by
+    // the thread that reads the word.
+    __device__ __forceinline__ void tail(unsigned char* slot, int64_t row) const {
+        const int j = words() - 1;
+        T* e = reinterpret_cast<T*>(slot + 16 * j);
+#pragma unroll 1
+        for (int i = 0; i < VEC; ++i) {
+            const int c = j * VEC + i - s;
+            if (c >= 0 && c < d) e[i] = __ldg(p + row * d + c);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    // the elements of such a word that belong to the row
+    __device__ __forceinline__ void store_part(T* out, int64_t row, int j, uint4 v) const {
+        T* o = reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(out) + at(row) + 16 * j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = j * VEC + i - s;
+            if (c < 0 || c >= d) continue;
+            if constexpr (sizeof(T) == 2)
+                o[i] = __ushort_as_bfloat16((unsigned short)(w[i / 2] >> (16 * (i & 1))));
+            else
+                o[i] = __uint_as_float(w[i]);
+        }
+    }
+};
+
+__device__ __forceinline__ uint4 masked(uint4 v, uint4 m) {
+    return make_uint4(v.x & m.x, v.y & m.y, v.z & m.z, v.w & m.w);
+}
+
+// ln_fwd_warp_kernel for such rows; gridDim.x is a multiple of 8
+template <typename T, int NV>
+__global__ void __launch_bounds__(256, WARP_BLOCKS<NV>)
+ln_fwd_shift_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int64_t Tn, int d,
+                    float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots,
+                    Limits lim) {
+    constexpr int TH = 256, VEC = Vec16<T>::VEC, HV = VEC / 2, PL = VEC / 4;
+    extern __shared__ float4 wb[];      // [w, b][NV][PL][32], then the warps' slots
+    __shared__ __align__(8) uint64_t bars[TH / 32][WARP_SLOTS];
+    __shared__ int abort_flag;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x < TH / 32 * WARP_SLOTS) ptx::mbar_init(ptx::smem_u32(&bars[0][0] + threadIdx.x), 1);
+    if (threadIdx.x == 0) abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncthreads();
+    pdl_launch_next();
+    pdl_wait();
+    const Shifted<T> sx(x, Tn, d, blockIdx.x);
+    const int64_t warps = (int64_t)gridDim.x * (TH / 32);
+    int64_t row = (int64_t)warp * gridDim.x + blockIdx.x;
+    unsigned char* ring = reinterpret_cast<unsigned char*>(wb + 2 * NV * PL * 32) + (size_t)warp * slots * sx.slot_bytes;
+    int left = lim.stop;
+    auto load = [&](int64_t r, int s) {
+        if (left == 0) return;
+        --left;
+        const uint32_t bar = ptx::smem_u32(&bars[warp][s]);
+        ptx::mbar_arrive_tx(bar, sx.bytes(r));
+        sx.load(r, ptx::smem_u32(ring) + s * sx.slot_bytes, bar);
+    };
+    if (lane == 0)
+        for (int s = 0; s < slots; ++s)
+            if (row + s * warps < Tn) load(row + s * warps, s);
+    bool ok = true;
+    int slot = 0;
+    uint32_t parity = 0;
+    for (int i = threadIdx.x; i < NV * 32 * VEC; i += TH) {
+        const int v = i / (32 * VEC), l = i / VEC % 32, e = i % VEC, c = i - sx.s;
+        const int at = ((v * PL + e / 4) * 32 + l) * 4 + e % 4;
+        reinterpret_cast<float*>(wb)[at] = w && c >= 0 && c < d ? __ldg(w + c) : 1.f;
+        reinterpret_cast<float*>(wb)[NV * 32 * VEC + at] = b && c >= 0 && c < d ? __ldg(b + c) : 0.f;
+    }
+    __syncthreads();
+    const float inv_d = 1.0f / (float)d;
+    // this lane's words at the ends of the row: word 0, and the last one in round vl; 1 in place of their
+    // elements that belong to the row, 0 of the others
+    const int nw = sx.words(), vl = (nw - 1) / 32;
+    const int j_lo = sx.s > 0 ? 1 : 0, j_hi = sx.spare() > 0 ? nw - 1 : nw;        // whole words
+    const bool first = lane == 0 && sx.s > 0, last = lane == (nw - 1) % 32 && sx.spare() > 0;
+    const uint4 mask0 = sx.mask(lane), mask1 = sx.mask(vl * 32 + lane);
+    float2 keep0[HV], keep1[HV];
+#pragma unroll
+    for (int e = 0; e < HV; ++e) {
+        auto in = [&](int j, int i) { return j * VEC + i - sx.s >= 0 && j * VEC + i - sx.s < d ? 1.f : 0.f; };
+        keep0[e] = make_float2(in(lane, 2 * e), in(lane, 2 * e + 1));
+        keep1[e] = make_float2(in(vl * 32 + lane, 2 * e), in(vl * 32 + lane, 2 * e + 1));
+    }
+    for (; row < Tn; row += warps) {
+        ok = wait_until(ptx::smem_u32(&bars[warp][slot]), parity, &abort_flag, lim.wait_ns) && ok;
+        unsigned char* xs = ring + (size_t)slot * sx.slot_bytes;
+        if (last && row == Tn - 1) sx.tail(xs, row);
+        uint4 raw[NV];
+        float2 a0 = both(0.f), a1 = both(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+        {
+            raw[v] = v * 32 + lane < nw ? *reinterpret_cast<const uint4*>(xs + 16 * (v * 32 + lane))
+                                        : make_uint4(0, 0, 0, 0);
+            if (v == 0) raw[v] = masked(raw[v], mask0);
+            if (v == vl) raw[v] = masked(raw[v], mask1);
+        }
+        __syncwarp();
+        if (lane == 0 && row + slots * warps < Tn) load(row + slots * warps, slot);
+        if (++slot == slots) {
+            slot = 0;
+            parity ^= 1u;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float2 f[HV];
+            pairs_of(raw[v], f);
+#pragma unroll
+            for (int e = 0; e < HV; e += 2) {
+                a0 = __fadd2_rn(a0, f[e]);
+                a1 = __fadd2_rn(a1, f[e + 1]);
+            }
+        }
+        float sum = (a0.x + a0.y) + (a1.x + a1.y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float mean = sum * inv_d;
+        a0 = a1 = both(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (v * 32 + lane >= nw) continue;
+            float2 f[HV];
+            pairs_of(raw[v], f);
+#pragma unroll
+            for (int e = 0; e < HV; ++e) {
+                f[e] = __fadd2_rn(f[e], both(-mean));
+                if (v == 0) f[e] = __fmul2_rn(f[e], keep0[e]);
+                if (v == vl) f[e] = __fmul2_rn(f[e], keep1[e]);
+                if (e & 1)
+                    a1 = __ffma2_rn(f[e], f[e], a1);
+                else
+                    a0 = __ffma2_rn(f[e], f[e], a0);
+            }
+        }
+        sum = (a0.x + a0.y) + (a1.x + a1.y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float rstd = 1.0f / sqrtf(fmaf(sum, inv_d, eps));
+        unsigned char* yr = reinterpret_cast<unsigned char*>(y) + sx.at(row);
+        uint4 end0 = make_uint4(0, 0, 0, 0), end1 = end0;      // words that are not wholly the row's
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int j = v * 32 + lane;
+            float2 f[HV];
+            pairs_of(raw[v], f);
+#pragma unroll
+            for (int h = 0; h < PL; ++h) {
+                const float4 wq = wb[(v * PL + h) * 32 + lane], bq = wb[((NV + v) * PL + h) * 32 + lane];
+                const float2 x0 = __fmul2_rn(__fadd2_rn(f[2 * h], both(-mean)), both(rstd));
+                const float2 x1 = __fmul2_rn(__fadd2_rn(f[2 * h + 1], both(-mean)), both(rstd));
+                f[2 * h] = __ffma2_rn(x0, make_float2(wq.x, wq.y), make_float2(bq.x, bq.y));
+                f[2 * h + 1] = __ffma2_rn(x1, make_float2(wq.z, wq.w), make_float2(bq.z, bq.w));
+            }
+            const uint4 o = vector_of(f);
+            if (j >= j_lo && j < j_hi) st_v4(yr + 16 * j, o);
+            if (v == 0) end0 = o;
+            if (v == vl) end1 = o;
+        }
+        if (first || last) {
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+                if (k ? last : first) sx.store_part(y, row, k ? nw - 1 : 0, k ? end1 : end0);
+        }
+        if (lane == 0 && mean_out) {
+            mean_out[row] = mean;
+            rstd_out[row] = rstd;
+        }
+    }
+    if (!ok) land();
+}
+
+// ln_bwd_ring_kernel for such rows, R at a time per block; gridDim.x is a multiple of 8
+template <typename T, int NV, int R, int TH>
+__global__ void __launch_bounds__(TH + 32, 1)
+ln_bwd_shift_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
+                    const float* __restrict__ rstd, const T* __restrict__ dy, int64_t Tn, int d, T* __restrict__ dx,
+                    float* __restrict__ part, bool late, int slots, Limits lim) {
+    constexpr int VEC = Vec16<T>::VEC, HV = VEC / 2;
+    extern __shared__ __align__(128) unsigned char smem[];      // slots of R rows of x, then of dy
+    __shared__ __align__(8) uint64_t bars[2 * MAX_SLOTS];
+    __shared__ int abort_flag;
+    __shared__ __align__(16) float buf[128 * R];
+    int phase = 0;
+    const int nthr = blockDim.x - 32, idx = threadIdx.x;
+    if (idx == 0) ring_init(bars, &abort_flag, slots, nthr >> 5);
+    __syncthreads();
+    pdl_launch_next();
+    const StreamOrder order(late);
+    Ring ring{bars, &abort_flag, slots, lim};
+    const Shifted<T> sx(x, Tn, d, blockIdx.x), sg(dy, Tn, d, blockIdx.x);
+    const int64_t step = (int64_t)gridDim.x * R;      // rows row, row + gridDim.x, .. of a batch
+    if (idx >= nthr) {
+        bool ok = true;
+        if (idx == nthr) {
+            int left = lim.stop;
+            for (int64_t row = blockIdx.x; row < Tn && left != 0; row += step, ring.next(), --left) {
+                if (!(ok = ring.wait(ring.empty(), ring.parity ^ 1u))) break;
+                uint32_t bytes = 0;
+                for (int r = 0; r < R && row + r * gridDim.x < Tn; ++r) bytes += 2 * sx.bytes(row + r * gridDim.x);
+                ptx::mbar_arrive_tx(ring.full(), bytes);
+                const uint32_t dst = ptx::smem_u32(smem) + ring.s * 2 * R * sx.slot_bytes;
+                for (int r = 0; r < R && row + r * gridDim.x < Tn; ++r) {
+                    sx.load(row + r * gridDim.x, dst + r * sx.slot_bytes, ring.full());
+                    sg.load(row + r * gridDim.x, dst + (R + r) * sx.slot_bytes, ring.full());
+                }
+            }
+            if (!ok) land();
+        }
+        __syncwarp();
+        return;
+    }
+    const float inv_d = 1.0f / (float)d;
+    float2 wv[NV][HV], dw[NV][HV], db[NV][HV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < HV; ++e) {
+            const int c = (v * nthr + idx) * VEC + 2 * e - sx.s;
+            wv[v][e].x = w && c >= 0 && c < d ? __ldg(w + c) : 1.f;
+            wv[v][e].y = w && c + 1 >= 0 && c + 1 < d ? __ldg(w + c + 1) : 1.f;
+            dw[v][e] = db[v][e] = both(0.f);
+        }
+    const int nw = sx.words(), j_lo = sx.s > 0 ? 1 : 0, j_hi = sx.spare() > 0 ? nw - 1 : nw;      // whole words: j_lo ..
+    const int vl = (nw - 1) / nthr;
+    const bool last = idx == (nw - 1) % nthr && sx.spare() > 0;
+    const uint4 mask0 = sx.mask(idx), mask1 = sx.mask(vl * nthr + idx);
+    float mu_n[R], rs_n[R];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t q = row + r * (int64_t)gridDim.x;
+            mu_n[r] = q < Tn ? __ldg(mean + q) : 0.f;
+            rs_n[r] = q < Tn ? __ldg(rstd + q) : 0.f;
+        }
+    };
+    fetch(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < Tn; row += step, ring.next()) {
+        float mu[R], rs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mu[r] = mu_n[r];
+            rs[r] = rs_n[r];
+        }
+        fetch(row + step);
+        ring.wait(ring.full(), ring.parity);
+        unsigned char* xs = smem + ring.s * 2 * R * sx.slot_bytes;
+        if (last) {
+#pragma unroll 1
+            for (int r = 0; r < R; ++r)
+                if (row + r * (int64_t)gridDim.x == Tn - 1) {
+                    sx.tail(xs + r * sx.slot_bytes, Tn - 1);
+                    sg.tail(xs + (R + r) * sx.slot_bytes, Tn - 1);
+                }
+        }
+        uint4 xr[R][NV], gr[R][NV];
+        float2 sa[R], sb[R];                         // sums of g, of g xh
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t q = row + r * (int64_t)gridDim.x;
+            sa[r] = sb[r] = both(0.f);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int j = v * nthr + idx;
+                xr[r][v] = gr[r][v] = make_uint4(0, 0, 0, 0);
+                if (q >= Tn || j >= nw) continue;
+                xr[r][v] = *reinterpret_cast<const uint4*>(xs + r * sx.slot_bytes + 16 * j);
+                gr[r][v] = *reinterpret_cast<const uint4*>(xs + (R + r) * sx.slot_bytes + 16 * j);
+                if (v == 0) {
+                    xr[r][v] = masked(xr[r][v], mask0);
+                    gr[r][v] = masked(gr[r][v], mask0);
+                }
+                if (v == vl) {
+                    xr[r][v] = masked(xr[r][v], mask1);
+                    gr[r][v] = masked(gr[r][v], mask1);
+                }
+                float2 xf[HV], gf[HV];
+                pairs_of(xr[r][v], xf);
+                pairs_of(gr[r][v], gf);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) {
+                    const float2 xh = __fmul2_rn(__fadd2_rn(xf[e], both(-mu[r])), both(rs[r]));
+                    const float2 g = __fmul2_rn(gf[e], wv[v][e]);
+                    dw[v][e] = __ffma2_rn(gf[e], xh, dw[v][e]);
+                    db[v][e] = __fadd2_rn(db[v][e], gf[e]);
+                    sa[r] = __fadd2_rn(sa[r], g);
+                    sb[r] = __ffma2_rn(g, xh, sb[r]);
+                }
+            }
+        }
+        float sums[2 * R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            sums[r] = sa[r].x + sa[r].y;
+            sums[R + r] = sb[r].x + sb[r].y;
+        }
+        __syncwarp();
+        if ((idx & 31) == 0) ptx::mbar_arrive(ring.empty());
+        if (!dx) continue;
+        group_sum<2 * R, 0>(sums, buf, phase, nthr);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t q = row + r * (int64_t)gridDim.x;
+            if (q >= Tn) break;
+            // dx = rs g w - (rs k) xh - rs a
+            const float2 a = both(-rs[r] * (sums[r] * inv_d)), k = both(-rs[r] * (sums[R + r] * inv_d) * rs[r]);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int j = v * nthr + idx;
+                if (j >= nw) continue;
+                float2 xf[HV], gf[HV];
+                pairs_of(xr[r][v], xf);
+                pairs_of(gr[r][v], gf);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) {
+                    const float2 t = __ffma2_rn(__fadd2_rn(xf[e], both(-mu[r])), k, a);
+                    gf[e] = __ffma2_rn(__fmul2_rn(gf[e], wv[v][e]), both(rs[r]), t);
+                }
+                const uint4 o = vector_of(gf);
+                if (j >= j_lo && j < j_hi)
+                    st_v4(reinterpret_cast<unsigned char*>(dx) + sx.at(q) + 16 * j, o);
+                else
+                    sx.store_part(dx, q, j, o);
+            }
+        }
+    }
+    if (!part) return;
+    float* pw = part + (int64_t)blockIdx.x * 2 * d;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = (v * nthr + idx) * VEC + e - sx.s;
+            if (c >= 0 && c < d) {
+                pw[c] = e & 1 ? dw[v][e / 2].y : dw[v][e / 2].x;
+                pw[d + c] = e & 1 ? db[v][e / 2].y : db[v][e / 2].x;
+            }
+        }
+}
+
+// out[c] = sum over the P blocks of part[p][c], c < 2 d: a block takes 32 columns, its 32 warps a
 // strided share of the rows each, eight loads in flight, added in a fixed order
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(1024)
 ln_cols_kernel(const float* __restrict__ part, int P, int d, float* __restrict__ dw, float* __restrict__ db) {
-    __shared__ float sm[16][33];
+    __shared__ float sm[32][33];
     pdl_launch_next();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane, ld = 2 * (int64_t)d;
     float s = 0.f;
     if (c < ld) {
-        for (int p = warp; p < P; p += 128) {
+        for (int p = warp; p < P; p += 256) {
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = p + 16 * j < P ? __ldcg(part + (int64_t)(p + 16 * j) * ld + c) : 0.f;
+            for (int j = 0; j < 8; ++j) v[j] = p + 32 * j < P ? __ldcg(part + (int64_t)(p + 32 * j) * ld + c) : 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += v[j];
         }
@@ -906,12 +1311,57 @@ ln_cols_kernel(const float* __restrict__ part, int P, int d, float* __restrict__
     __syncthreads();
     if (warp == 0 && c < ld) {
 #pragma unroll
-        for (int k = 1; k < 16; ++k) s += sm[k][lane];
+        for (int k = 1; k < 32; ++k) s += sm[k][lane];
         if (c < d) {
             if (dw) dw[c] = s;
         } else if (db) {
             db[c - d] = s;
         }
+    }
+}
+
+// dw_c = sum_t dy_c xh_c and db_c = sum_t dy_c straight from the rows: 32 columns per block, a 32nd of
+// the rows per warp, four of them in flight, added in a fixed order
+template <typename T>
+__global__ void __launch_bounds__(1024)
+ln_few_cols_kernel(const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
+                   const T* __restrict__ dy, int Tn, int d, float* __restrict__ dw, float* __restrict__ db) {
+    constexpr int U = 4;
+    __shared__ float sm[2][32][33];
+    // in this order: the row kernel that starts early behind this one reads what this one waited for
+    pdl_wait();
+    pdl_launch_next();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float sw = 0.f, sb = 0.f;
+    if (c < d) {
+        for (int t = warp; t < Tn; t += 32 * U) {
+            float xv[U], gv[U], mu[U], rs[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t row = t + 32 * j;
+                const bool in = row < Tn;
+                xv[j] = in ? to_f32(__ldg(x + row * d + c)) : 0.f;
+                gv[j] = in ? to_f32(__ldg(dy + row * d + c)) : 0.f;
+                mu[j] = in ? __ldg(mean + row) : 0.f;
+                rs[j] = in ? __ldg(rstd + row) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                sw = fmaf(gv[j], (xv[j] - mu[j]) * rs[j], sw);
+                sb += gv[j];
+            }
+        }
+    }
+    sm[0][warp][lane] = sw;
+    sm[1][warp][lane] = sb;
+    __syncthreads();
+    float* const out = warp == 0 ? dw : db;
+    if (warp < 2 && c < d && out) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s += sm[warp][k][lane];
+        out[c] = s;
     }
 }
 
@@ -958,7 +1408,7 @@ cudaError_t bwd(const LnArgs& a, int* blocks) {
     if (cap > bwd_blocks(a.d)) cap = bwd_blocks(a.d);
     *blocks = (int)(want < cap ? want : cap);
     return launch_pdl(kern, dim3((unsigned)*blocks), dim3(threads), smem, a.stream, static_cast<const T*>(a.x), a.w,
-                      a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part);
+                      a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part, a.late);
 }
 
 std::atomic<unsigned long long> g_wait_ns{1000000000ull};      // 1 s per wait
@@ -1017,7 +1467,7 @@ cudaError_t bwd_ring(const LnArgs& a, int* blocks) {
     *blocks = (int)(want < cap ? want : cap);
     return launch_pdl(kern, dim3((unsigned)*blocks), dim3(r.threads), r.bytes, a.stream, static_cast<const T*>(a.x),
                       a.w, a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part,
-                      r.slots, limits());
+                      a.late, r.slots, limits());
 }
 
 template <typename T, int NV>
@@ -1040,9 +1490,55 @@ cudaError_t fwd_warp(const LnArgs& a) {
                       limits());
 }
 
-// The layout of a row by its length in vectors: 8, 16 or 32 lanes with one vector each, 32 with two,
-// a block with two (then four) vectors per thread above that.  At most one row per SM takes a register
+template <typename T, int NV>
+cudaError_t fwd_shift(const LnArgs& a) {
+    constexpr int TH = 256;
+    auto kern = ln_fwd_shift_kernel<T, NV>;
+    const size_t wb = (size_t)2 * NV * 32 * Vec16<T>::VEC * 4;
+    const size_t slot = (size_t)(TH / 32) * ((a.d * sizeof(T) + 15) / 16 * 16 + 16);
+    int slots = (int)((204800 / WARP_BLOCKS<NV> - wb) / slot);
+    slots = slots < 1 ? 1 : slots > WARP_SLOTS ? WARP_SLOTS : slots;
+    const size_t smem = wb + slots * slot;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.T + TH / 32 - 1) / (TH / 32);
+    int cap;
+    e = resident(kern, TH, smem, want, &cap);
+    if (e != cudaSuccess) return e;
+    const int blocks = (int)(want < cap ? want : cap) / 8 * 8;      // at least 16 rows per SM: never 0
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(TH), smem, a.stream,
+                      static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd, slots,
+                      limits());
+}
+
+template <typename T, int NV, int R, int TH>
+cudaError_t bwd_shift(const LnArgs& a, int* blocks) {
+    constexpr int VEC = Vec16<T>::VEC;
+    auto kern = ln_bwd_shift_kernel<T, NV, R, TH>;
+    const int words = (a.d + 2 * VEC - 2) / VEC, nthr = ((words + NV - 1) / NV + 31) / 32 * 32;
+    const size_t slot = (size_t)2 * R * ((a.d * sizeof(T) + 15) / 16 * 16 + 16);
+    int slots = (int)(204800 / (nthr >= 320 ? 2 : nthr <= 64 ? 10 : 640 / nthr) / slot);
+    slots = slots < 2 ? 2 : slots > MAX_SLOTS ? MAX_SLOTS : slots;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(slots * slot));
+    if (e != cudaSuccess) return e;
+    const int64_t want = (a.T + 3) / 4;
+    int cap;
+    e = resident(kern, nthr + 32, slots * slot, want, &cap);
+    if (e != cudaSuccess) return e;
+    if (cap > bwd_blocks(a.d)) cap = bwd_blocks(a.d);
+    *blocks = (int)(want < cap ? want : cap) / 8 * 8;       // at least 16 rows per SM: never 0
+    return launch_pdl(kern, dim3((unsigned)*blocks), dim3(nthr + 32), slots * slot, a.stream, static_cast<const T*>(a.x),
+                      a.w, a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d, static_cast<T*>(a.dx), a.part,
+                      a.late, slots, limits());
+}
+
+// The layout of a row by its length in vectors: 8, 16 or 32 lanes with one vector each, 32 with two, a
+// warp with up to 16, a block with two (then four) per thread.  At most one row per SM takes a register
 // kernel.
+// Rows that are not a multiple of 16 bytes take the shift kernels from 16 rows per SM on.  T = 16384,
+// bf16: d = 4095 forward 68 us against 132 one element at a time, backward 123 against 165; d = 2559
+// backward 86 against 104.  With fewer rows filling the ring costs more than it hides: T = 1200, d = 1037
+// forward 7.4 against 5.8 us, T = 2400 7.9 against 9.4.
 template <typename T>
 cudaError_t fwd_t(const LnArgs& a, int sms) {
     constexpr int V = Vec16<T>::VEC;
@@ -1063,6 +1559,16 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
         if (c <= 1024) return fwd_ring<T, 2, 2, 0, 512>(a);
         if (c <= 2048) return fwd_ring<T, 4, 1, 0, 512>(a);
     } else {
+        // vectors that the words around a row may take
+        const int c = ((int)sizeof(T) * a.d + 30) / 16;
+        if (a.T >= 16 * sms && a.d > 256 && c <= 544 && rows16(a.x) && rows16(a.y)) {
+            if (c <= 128) return fwd_shift<T, 4>(a);
+            if (c <= 192) return fwd_shift<T, 6>(a);
+            if (c <= 256) return fwd_shift<T, 8>(a);
+            if (c <= 320) return fwd_shift<T, 10>(a);
+            if (c <= 384) return fwd_shift<T, 12>(a);
+            return fwd_shift<T, 17>(a);
+        }
         if (a.d <= 256) return fwd<T, 1, 8, 2, true>(a);
         if (a.d <= 4096) return fwd<T, 1, 8, 2, false>(a);
         if (a.d <= 8192) return fwd<T, 1, 16, 1, false>(a);
@@ -1074,6 +1580,10 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
                       static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
 }
 
+// As forward, but a block has two vectors per thread and two rows at a time.  320 to 480 vectors: three
+// and one, because two need six warps or more, whose registers leave room for one block per SM only (T =
+// 16384, bf16, d = 2816: 61 us against 79, d = 3584: 75 against 80; d = 4096 needs six warps either way:
+// 85 with two, 115 with three).
 template <typename T>
 cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
     constexpr int V = Vec16<T>::VEC;
@@ -1085,12 +1595,19 @@ cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
         if (c <= 16) return bwd_ring<T, 1, 2, 16, W>(a, blocks);
         if (c <= 32) return bwd_ring<T, 1, 2, 32, W>(a, blocks);
         if (c <= 64) return bwd_ring<T, 2, 1, 32, W>(a, blocks);
+        if (c > 320 && c <= 480) return bwd_ring<T, 3, 1, 0, 256>(a, blocks);
         if (c <= 512) return bwd_ring<T, 2, 2, 0, 256>(a, blocks);
         if (c <= 1024) return bwd_ring<T, 2, 1, 0, 512>(a, blocks);
         if constexpr (V == 4) {
             if (c <= 2048) return bwd_ring<T, 4, 1, 0, 512>(a, blocks);
         }
     } else {
+        const int c = ((int)sizeof(T) * a.d + 30) / 16;
+        if (a.T >= 16 * sms && a.d > 256 && c <= 1024 && rows16(a.x) && rows16(a.dy) && rows16(a.dx)) {
+            if (c > 320 && c <= 480) return bwd_shift<T, 3, 1, 256>(a, blocks);
+            if (c <= 512) return bwd_shift<T, 2, 2, 256>(a, blocks);
+            return bwd_shift<T, 2, 1, 512>(a, blocks);
+        }
         if (a.d <= 256) return bwd<T, 1, 8, 1, true>(a, blocks);
         if (a.d <= 4096) return bwd<T, 1, 8, 1, false>(a, blocks);
         if (a.d <= 8192) return bwd<T, 1, 16, 1, false>(a, blocks);
@@ -1102,7 +1619,7 @@ cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
     *blocks = (int)(a.T < cap ? a.T : cap);
     return launch_pdl(ln_bwd_long_kernel<T>, dim3((unsigned)*blocks), dim3(1024), 0, a.stream,
                       static_cast<const T*>(a.x), a.w, a.mean, a.rstd, static_cast<const T*>(a.dy), a.T, a.d,
-                      static_cast<T*>(a.dx), a.part);
+                      static_cast<T*>(a.dx), a.part, a.late);
 }
 
 }  // namespace
@@ -1119,15 +1636,28 @@ cudaError_t launch_layer_norm(const LnArgs& a) {
     return a.dt == BF16 ? fwd_t<__nv_bfloat16>(a, di.sm_count) : fwd_t<float>(a, di.sm_count);
 }
 
-cudaError_t launch_layer_norm_backward(const LnArgs& a) {
+cudaError_t launch_layer_norm_backward(const LnArgs& args) {
     DeviceInfo di;
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
+    LnArgs a = args;
+    a.late = a.part && a.T <= FEW_ROWS;
+    if (a.late) {
+        const dim3 grid((unsigned)(((int64_t)a.d + 31) / 32));
+        e = a.dt == BF16 ? launch_pdl(ln_few_cols_kernel<__nv_bfloat16>, grid, dim3(1024), 0, a.stream,
+                                      static_cast<const __nv_bfloat16*>(a.x), a.mean, a.rstd,
+                                      static_cast<const __nv_bfloat16*>(a.dy), (int)a.T, a.d, a.dw, a.db)
+                         : launch_pdl(ln_few_cols_kernel<float>, grid, dim3(1024), 0, a.stream,
+                                      static_cast<const float*>(a.x), a.mean, a.rstd,
+                                      static_cast<const float*>(a.dy), (int)a.T, a.d, a.dw, a.db);
+        a.part = nullptr;
+        if (e != cudaSuccess || !a.dx) return e;
+    }
     int blocks = 0;
     e = a.dt == BF16 ? bwd_t<__nv_bfloat16>(a, di.sm_count, &blocks) : bwd_t<float>(a, di.sm_count, &blocks);
     if (e != cudaSuccess || !a.part) return e;
     const unsigned grid = (unsigned)((2 * (int64_t)a.d + 31) / 32);
-    return launch_pdl(ln_cols_kernel, dim3(grid), dim3(512), 0, a.stream, a.part, blocks, a.d, a.dw, a.db);
+    return launch_pdl(ln_cols_kernel, dim3(grid), dim3(1024), 0, a.stream, a.part, blocks, a.d, a.dw, a.db);
 }
 
 void layer_norm_set_stop(int stop, unsigned long long wait_ns) {

@@ -16,6 +16,9 @@ EPS = 1e-5
 
 SHAPES = [(1, 1), (1, 4096), (3, 2), (5, 7), (17, 8), (40, 64), (33, 250), (257, 256), (100, 257), (64, 512),
           (70, 520), (31, 1000), (700, 1024), (301, 1037), (149, 2560), (1200, 4096), (9, 4095), (150, 4104),
+          # odd widths, many rows: rows at every offset within 16 bytes, and a last row that ends inside a word
+          (2375, 257), (2403, 260), (2401, 1025), (2369, 1532), (2500, 2047), (2373, 2562), (2427, 2819), (2379, 4090),
+          (2399, 4102), (2377, 201), (513, 1030), (512, 515),
           (3, 8192), (160, 8191), (5, 8200), (2, 16384), (3, 20001), (2, 40000)]
 
 
