@@ -22,11 +22,13 @@ constexpr int DZ_BLOCKS = 16 * 148;    // blocks wanted, sixteen per SM of a 148
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// runs of tokens of the elementwise step, each with a row of column sums
+// Runs of tokens of the elementwise step, each with a row of column sums: two tokens per thread at least
+// (one: T = 4096, N = 1024 11.4 us against 7.9, T = 16384, N = 256 15.5 against 11.2; four: no gain but
+// without an activation, T = 1000, N = 4096 9.2 against 7.4)
 int64_t dz_runs(int64_t T, int N) {
     const int64_t col_blocks = ((int64_t)N + 255) / 256;
     const int64_t want = std::max<int64_t>(1, DZ_BLOCKS / col_blocks);
-    return std::min(want, (T + DZ_ROWS - 1) / DZ_ROWS);
+    return std::min(want, (T + 2 * DZ_ROWS - 1) / (2 * DZ_ROWS));
 }
 
 // Loads of VEC columns at (t, c): 16-byte rows, or bf16 rows wherever they lie (SHIFT)
@@ -42,8 +44,8 @@ __device__ __forceinline__ void dz_load(const T* __restrict__ p, int64_t t, int6
 }
 
 // A thread takes VEC columns of a token at a time: its two loads, and many blocks per SM in place of
-// more of them (T = N = 16384 with GELU: four tokens at a time took 540 us, one 325).  dz null: column
-// sums only; part null: no sums.
+// more of them (T = N = 16384 with GELU: four tokens at a time took 510 us, one 300, 5.4 TB/s; the
+// sums alone, without dz, 216).  dz null: column sums only; part null: no sums.
 template <typename T, int VEC, int ACT, bool SHIFT>
 __global__ void __launch_bounds__(DZ_COLS* DZ_ROWS)
 dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, int64_t run, T* __restrict__ dz,
@@ -89,22 +91,30 @@ dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int64_t Tn, int N, 
     }
 }
 
-// out[c] = sum over P rows of part, in a fixed order
-__global__ void __launch_bounds__(256)
+// out[c] = sum over P rows of part, in a fixed order: 32 columns per block, a 32nd of the rows per warp,
+// eight of them in flight
+__global__ void __launch_bounds__(1024)
 sum_rows_kernel(const float* __restrict__ part, int64_t P, int N, float* __restrict__ out) {
-    __shared__ float sm[8][33];
+    constexpr int U = 8;
+    __shared__ float sm[32][33];
     pdl_launch_next();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < N)
-        for (int64_t p = warp; p < P; p += 8) s += part[p * N + c];
+        for (int64_t p = warp; p < P; p += 32 * U) {
+            float v[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) v[j] = p + 32 * j < P ? __ldcg(part + (p + 32 * j) * N + c) : 0.f;
+#pragma unroll
+            for (int j = 0; j < U; ++j) s += v[j];
+        }
     sm[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < N) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k) s += sm[k][lane];
+        for (int k = 1; k < 32; ++k) s += sm[k][lane];
         out[c] = s;
     }
 }
@@ -143,7 +153,7 @@ cudaError_t launch_dz(const LinearArgs& a, void* dz, int64_t ld, float* part) {
     else
         e = start_dz<T, 1, false>(a, dz, ld, run, rows, sums);
     if (e == cudaSuccess && a.dbias && rows > 1)
-        e = launch_pdl(sum_rows_kernel, dim3((unsigned)((a.N + (int64_t)31) / 32)), dim3(256), 0, a.stream, part,
+        e = launch_pdl(sum_rows_kernel, dim3((unsigned)((a.N + (int64_t)31) / 32)), dim3(1024), 0, a.stream, part,
                        rows, a.N, a.dbias);
     return e;
 }
