@@ -119,6 +119,48 @@ def test_constant_rows_and_non_finite_rows():
 
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(2400, 515), (2371, 1537), (600, 515), (300, 520)])
+def test_non_finite_rows_stay_in_their_rows(T, d, dt):
+    # rows that share a 16-byte word with their neighbours among them
+    x, w, b, dy = _case(T, d, dt, 8)
+    y0, mean, rstd = _fwd(x, w, b)
+    dx0 = _bwd(x, w, mean, rstd, dy)[0]
+    bad = [1, 8, T // 2, T - 1]
+    for k, t in enumerate(bad):
+        x[t, :: d - 1] = float("inf") if k % 2 else float("nan")      # the row's first and last element
+        dy[t, :: d - 1] = float("nan")
+    y1, mean1, rstd1 = _fwd(x, w, b)
+    dx1 = _bwd(x, w, mean1, rstd1, dy)[0]
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[bad] = False
+    assert torch.equal(y1[keep], y0[keep]) and torch.equal(dx1[keep], dx0[keep])
+    assert torch.equal(mean1[keep], mean[keep]) and torch.equal(rstd1[keep], rstd[keep])
+    assert not torch.isfinite(y1[bad]).any() and not torch.isfinite(dx1[bad]).any()
+
+
+@pytest.mark.parametrize("T,d", [(3, 4096), (140, 1024), (500, 2560), (512, 1037), (513, 1037)])
+def test_backward_calls_in_a_row(T, d):
+    # each call's dx is the next one's dy, into buffers used in turn: nothing may start before what it
+    # reads is there, nor write what is still read
+    x, w, b, dy = _dev(*_case(T, d, BF, 9))
+    _, mean, rstd = _fwd(x, w, b)
+    n = 24
+    ws = torch.empty(mhc.mhc_layer_norm_backward_workspace_bytes(T, d), dtype=torch.uint8, device="cuda")
+    res = []
+    for apart in (True, False):
+        g, h = dy.clone(), torch.empty_like(dy)
+        dw, db = torch.empty(n, d, device="cuda"), torch.empty(n, d, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(n):
+            mhc.mhc_layer_norm_backward(x, w, mean, rstd, g, h, dw[i], db[i], ws)
+            if apart:
+                torch.cuda.synchronize()
+            g, h = h, g
+        res.append((g, dw, db))
+    assert all(torch.equal(p, q) for p, q in zip(*res))
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("T,d", [(7, 64), (50, 1000), (150, 4096), (3, 8000)])
 def test_unaligned_buffers(T, d, dt):
     x, w, b, dy = _case(T, d, dt, 4)
@@ -156,7 +198,8 @@ def test_gradient_against_differences():
         assert abs((f(x, w, b.double() + e) - f(x, w, b.double() - e)) / (2 * h) - float(db[c])) < 1e-5
 
 
-@pytest.mark.parametrize("T,d,dt", [(37, 64, BF), (301, 1037, F32), (150, 2560, BF), (9, 8200, BF), (3, 9001, F32)])
+@pytest.mark.parametrize("T,d,dt", [(37, 64, BF), (301, 1037, F32), (150, 2560, BF), (9, 8200, BF), (3, 9001, F32),
+                                    (2373, 1037, BF), (2401, 515, F32), (2369, 2563, BF)])
 def test_writes_stay_inside_the_outputs(T, d, dt):
     x, w, b, dy = _dev(*_case(T, d, dt, 6))
     res = []
