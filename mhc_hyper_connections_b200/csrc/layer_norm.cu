@@ -804,7 +804,10 @@ ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
         ring.wait(ring.full(), ring.parity);
         const T* xs = reinterpret_cast<const T*>(smem + (int64_t)ring.s * 2 * B * row_bytes) + (int64_t)first * d;
         const T* gs = xs + (int64_t)B * d;
-        uint4 xr[R][NV], gr[R][NV];
+        // x waits as it was stored, g as fp32: unpacking dy again costs more than the registers (T = 16384, d =
+        // 4096: 81 us against 77)
+        uint4 xr[R][NV];
+        float2 gk[R][NV][HV];
         float2 sg[R], sx[R];                         // sums of g, of g xh
 #pragma unroll
         for (int r = 0; r < R; ++r) sg[r] = sx[r] = both(0.f);
@@ -814,17 +817,16 @@ ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
             if (c >= d) continue;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const bool in = i * B + first + r < Tn;      // else the slot's last contents
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                xr[r][v] = in ? *reinterpret_cast<const uint4*>(xs + (int64_t)r * d + c) : zero;
-                gr[r][v] = in ? *reinterpret_cast<const uint4*>(gs + (int64_t)r * d + c) : zero;
+                if (i * B + first + r >= Tn) break;          // the slot's last contents
+                xr[r][v] = *reinterpret_cast<const uint4*>(xs + (int64_t)r * d + c);
+                const uint4 graw = *reinterpret_cast<const uint4*>(gs + (int64_t)r * d + c);
                 float2 xf[HV], gf[HV];
                 pairs_of(xr[r][v], xf);
-                pairs_of(gr[r][v], gf);
+                pairs_of(graw, gf);
 #pragma unroll
                 for (int e = 0; e < HV; ++e) {
                     const float2 xh = __fmul2_rn(__fadd2_rn(xf[e], both(-mu[r])), both(rs[r]));
-                    const float2 g = __fmul2_rn(gf[e], wv[v][e]);
+                    const float2 g = gk[r][v][e] = __fmul2_rn(gf[e], wv[v][e]);
                     dw[v][e] = __ffma2_rn(gf[e], xh, dw[v][e]);
                     db[v][e] = __fadd2_rn(db[v][e], gf[e]);
                     sg[r] = __fadd2_rn(sg[r], g);
@@ -854,11 +856,10 @@ ln_bwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
                 const float2 a = both(-rs[r] * (sums[r] * inv_d)), q = both(-rs[r] * (sums[R + r] * inv_d) * rs[r]);
                 float2 xf[HV], gf[HV];
                 pairs_of(xr[r][v], xf);
-                pairs_of(gr[r][v], gf);
 #pragma unroll
                 for (int e = 0; e < HV; ++e) {
                     const float2 t = __ffma2_rn(__fadd2_rn(xf[e], both(-mu[r])), q, a);
-                    gf[e] = __ffma2_rn(__fmul2_rn(gf[e], wv[v][e]), both(rs[r]), t);
+                    gf[e] = __ffma2_rn(gk[r][v][e], both(rs[r]), t);
                 }
                 st_v4(dx + row * d + c, vector_of(gf));
             }
@@ -1120,7 +1121,8 @@ ln_fwd_shift_kernel(const T* __restrict__ x, const float* __restrict__ w, const 
     if (!ok) land();
 }
 
-// ln_bwd_ring_kernel for such rows, R at a time per block; gridDim.x is a multiple of 8
+// ln_bwd_ring_kernel for such rows, R at a time per block; gridDim.x is a multiple of 8.  g is formed twice:
+// the masks leave no registers to keep it in (T = 16384, d = 4081, bf16: 121 us, 136 with g kept)
 template <typename T, int NV, int R, int TH>
 __global__ void __launch_bounds__(TH + 32, 1)
 ln_bwd_shift_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
@@ -1582,8 +1584,8 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
 
 // As forward, but a block has two vectors per thread and two rows at a time.  320 to 480 vectors: three
 // and one, because two need six warps or more, whose registers leave room for one block per SM only (T =
-// 16384, bf16, d = 2816: 61 us against 79, d = 3584: 75 against 80; d = 4096 needs six warps either way:
-// 85 with two, 115 with three).
+// 16384, bf16, d = 2816: 60 us against 79, d = 3584: 71 against 80; d = 4096 needs six warps either way:
+// 77 with two, 115 with three).
 template <typename T>
 cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
     constexpr int V = Vec16<T>::VEC;
