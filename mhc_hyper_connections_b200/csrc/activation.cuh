@@ -60,7 +60,10 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
         return z > 0.f ? 1.0f - tail : tail;
     } else {
         e = expf(-0.5f * z * z);
-        return 0.5f * (1.0f + erff(z * kSqrtHalf));
+        // the small side from erfc, so that it keeps its relative accuracy (1 + erf cancels there: off by a
+        // fifth at z = -5)
+        const float tail = 0.5f * erfcf(fabsf(z) * kSqrtHalf);
+        return z > 0.f ? 1.0f - tail : (z != z ? z : tail);
     }
 }
 
