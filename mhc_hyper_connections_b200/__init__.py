@@ -452,36 +452,53 @@ def mhc_backward_noalloc(X, F_out, phi, b_pre, b_post, b_res, alpha_pre, alpha_p
     _check(st, "mhc_backward_noalloc")
 
 
-def _rows(where, name, t):
+_torch = None
+
+
+def _bind_torch():
+    """torch, kept for the sub-layer operators: an import statement per helper costs more than their checks."""
+    global _torch
     import torch
+    _torch = torch
+    return torch
+
+
+def _rows(where, name, t):
+    torch = _torch or _bind_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{where}: {name} must be a torch tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{where}: {name} must be two-dimensional, has shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{where}: {name} must be two-dimensional, has shape {tuple(shape)}")
+    return shape
 
 
 def _pointers(where, dev, specs):
-    """Device pointers of tensor arguments given as (name, tensor or None, shape, dtype).  Every shape
-    is checked first (the C ABI sees only pointers, so a smaller tensor would be read or written past
-    its end), then device, dtype and contiguity."""
-    import torch
+    """Device pointers of tensor arguments given as (name, tensor or None, shape, dtype); the C ABI sees
+    only pointers, so a smaller tensor would be read or written past its end.  A call for one token takes
+    about as long on the host as on the device, so good arguments are walked once, by their cheapest tests."""
+    Tensor, index, out = _torch.Tensor, dev.index, []
+    for _, t, shape, dtype in specs:
+        if t is None:
+            out.append(0)
+        elif (isinstance(t, Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == index
+              and t.is_contiguous()):
+            out.append(t.data_ptr())
+        else:
+            return _refuse(where, dev, specs)
+    return out
+
+
+def _refuse(where, dev, specs):
+    """Raise for the first bad argument, naming it: every shape first, then device, contiguity and dtype."""
     for name, t, shape, _ in specs:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, _torch.Tensor):
             raise TypeError(f"{where}: {name} must be a torch tensor")
         if t.shape != shape:
             raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    out = []
-    for name, t, _, dtype in specs:
-        if t is None:
-            out.append(0)
-        elif t.dtype == dtype and t.device == dev and t.is_cuda and t.is_contiguous():
-            out.append(t.data_ptr())
-        else:
-            out.append(_ptr(t, name, dtype, dev))      # raises, naming the tensor
-    return out
+    return [_ptr(t, name, dtype, dev) for name, t, _, dtype in specs]
 
 
 def _workspace(workspace, dev):
@@ -493,12 +510,12 @@ def _workspace(workspace, dev):
 
 def _call(where, fn, dev, stream, args):
     """fn(*args, stream) with `dev` current, on the given or the current stream."""
-    import torch
+    torch = _torch
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(dev.index)      # current_stream() without its object
     else:
         s = _stream(stream, dev)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         st = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -512,12 +529,11 @@ def mhc_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
 
     x [T, d] (bf16/fp32); weight and bias [d] fp32, either may be None (1 and 0); written in
     place: y [T, d] (x's dtype) and, for training, mean and rstd [T] fp32 (both or neither)."""
-    import torch
     where = "mhc_layer_norm"
-    T, d = _rows(where, "x", x)
-    dt, xt, f32, dev = _dt(x), x.dtype, torch.float32, x.device
+    T, d = shape = _rows(where, "x", x)
+    dt, xt, f32, dev = _dt_of(x.dtype), x.dtype, _torch.float32, x.device
     px, pw, pb, py, pm, pr = _pointers(where, dev, (
-        ("x", x, x.shape, xt), ("weight", weight, (d,), f32), ("bias", bias, (d,), f32), ("y", y, x.shape, xt),
+        ("x", x, shape, xt), ("weight", weight, (d,), f32), ("bias", bias, (d,), f32), ("y", y, shape, xt),
         ("mean", mean, (T,), f32), ("rstd", rstd, (T,), f32)))
     _call(where, load_library().mhc_layer_norm, dev, stream, (px, pw, pb, T, d, float(eps), dt, py, pm, pr))
 
@@ -532,13 +548,12 @@ def mhc_layer_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, works
     and dbias [d] fp32; each may be None (not wanted).  mean and rstd [T] as mhc_layer_norm wrote
     them.  workspace: a CUDA tensor of mhc_layer_norm_backward_workspace_bytes(T, d) bytes; None
     will do when neither dweight nor dbias is wanted."""
-    import torch
     where = "mhc_layer_norm_backward"
-    T, d = _rows(where, "x", x)
-    dt, xt, f32, dev = _dt(x), x.dtype, torch.float32, x.device
+    T, d = shape = _rows(where, "x", x)
+    dt, xt, f32, dev = _dt_of(x.dtype), x.dtype, _torch.float32, x.device
     px, pw, pm, pr, pg, pdx, pdw, pdb = _pointers(where, dev, (
-        ("x", x, x.shape, xt), ("weight", weight, (d,), f32), ("mean", mean, (T,), f32), ("rstd", rstd, (T,), f32),
-        ("dy", dy, x.shape, xt), ("dx", dx, x.shape, xt), ("dweight", dweight, (d,), f32),
+        ("x", x, shape, xt), ("weight", weight, (d,), f32), ("mean", mean, (T,), f32), ("rstd", rstd, (T,), f32),
+        ("dy", dy, shape, xt), ("dx", dx, shape, xt), ("dweight", dweight, (d,), f32),
         ("dbias", dbias, (d,), f32)))
     ws, nbytes = _workspace(workspace, dev)
     _call(where, load_library().mhc_layer_norm_backward, dev, stream,
@@ -546,7 +561,7 @@ def mhc_layer_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, works
 
 
 def _dt_of(dtype) -> int:
-    import torch
+    torch = _torch or _bind_torch()
     if isinstance(dtype, int):
         return dtype
     if dtype == torch.bfloat16:
@@ -569,13 +584,12 @@ def mhc_linear(x, W, bias, y, act: int = ACT_NONE, residual=None, z=None, worksp
     ACT_GELU_TANH, ACT_SILU.  z, when given, is written: mhc_linear_backward needs it if there is
     an activation.  workspace: a CUDA tensor of mhc_linear_workspace_bytes(T, K, N, dtype) bytes;
     None will do when that is 0."""
-    import torch
     where = "mhc_linear"
-    T, K = _rows(where, "x", x)
+    T, K = shape = _rows(where, "x", x)
     N = _rows(where, "W", W)[0]
-    dt, xt, dev, out = _dt(x), x.dtype, x.device, (T, N)
+    dt, xt, f32, dev, out = _dt_of(x.dtype), x.dtype, _torch.float32, x.device, (T, N)
     px, pw, pb, pr, py, pz = _pointers(where, dev, (
-        ("x", x, x.shape, xt), ("W", W, (N, K), xt), ("bias", bias, (N,), torch.float32),
+        ("x", x, shape, xt), ("W", W, (N, K), xt), ("bias", bias, (N,), f32),
         ("residual", residual, out, xt), ("y", y, out, xt), ("z", z, out, xt)))
     ws, nbytes = _workspace(workspace, dev)
     _call(where, load_library().mhc_linear, dev, stream,
@@ -593,14 +607,13 @@ def mhc_linear_backward(x, W, z, dy, dx, dW, dbias, workspace, act: int = ACT_NO
     None (not wanted).  The residual's gradient is dy.  z [T, N] as mhc_linear wrote it; None will
     do for ACT_NONE.  workspace: a CUDA tensor of mhc_linear_backward_workspace_bytes(T, K, N,
     dtype) bytes."""
-    import torch
     where = "mhc_linear_backward"
-    T, K = _rows(where, "x", x)
+    T, K = shape = _rows(where, "x", x)
     N = _rows(where, "W", W)[0]
-    dt, xt, dev, out = _dt(x), x.dtype, x.device, (T, N)
+    dt, xt, f32, dev, out = _dt_of(x.dtype), x.dtype, _torch.float32, x.device, (T, N)
     px, pw, pz, pg, pdx, pdw, pdb = _pointers(where, dev, (
-        ("x", x, x.shape, xt), ("W", W, (N, K), xt), ("z", z, out, xt), ("dy", dy, out, xt), ("dx", dx, x.shape, xt),
-        ("dW", dW, (N, K), xt), ("dbias", dbias, (N,), torch.float32)))
+        ("x", x, shape, xt), ("W", W, (N, K), xt), ("z", z, out, xt), ("dy", dy, out, xt), ("dx", dx, shape, xt),
+        ("dW", dW, (N, K), xt), ("dbias", dbias, (N,), f32)))
     ws, nbytes = _workspace(workspace, dev)
     _call(where, load_library().mhc_linear_backward, dev, stream,
           (px, pw, pz, T, K, N, int(act), dt, pg, pdx, pdw, pdb, ws, nbytes))
