@@ -220,6 +220,7 @@ struct GemmArgs {
     Act act;
     void* D;
     void* z;
+    float* part;                 // of the tensor-core kernels: gemm_tc_part_bytes or gemm_f32_part_bytes
     DType dt;
     cudaStream_t stream;
 };
@@ -240,6 +241,10 @@ struct F32Planes {
     int64_t lda, ldb, a_plane, b_plane;
 };
 cudaError_t launch_gemm_f32(const GemmArgs& a, const F32Planes& f);
+// Scratch of the two, 256-byte aligned, and the modelled time of the second in us.
+size_t gemm_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool a_mn);
+size_t gemm_f32_part_bytes(int64_t M, int64_t N, int64_t K, bool a_mn);
+double gemm_f32_time(int64_t M, int64_t N, int64_t K, bool a_mn);
 cudaError_t linear_tc_status(unsigned* out, bool clear);
 void linear_tc_set_stop(int stop, unsigned long long wait_ns);      // as layer_norm_set_stop, in stages per CTA
 

@@ -246,16 +246,23 @@ cudaError_t split_rows(const SplitJob& a, const SplitJob& b, cudaStream_t s) {
     return launch_pdl(split_rows_kernel, dim3(SPLIT_BLOCKS, b.rows ? 2 : 1), dim3(256), 0, s, a, b);
 }
 
-// fp32 products that go to the tensor cores: those whose time on CUDA cores exceeds what the parts
-// cost to make
-bool parts_pay(int64_t T, int K, int N) {
-    return T > 64 && T < ((int64_t)1 << 31) - 1024 && (double)T * K * N >= 1e9;
+// fp32 products that go to the tensor cores: those whose time on CUDA cores exceeds that of the parts and
+// their products, by these times in us (measured, operands in L2): CUDA cores 7 us and 27 TFLOP/s; the parts
+// 10 bytes per element at 5.5 TB/s and 8.5 us for their launch and the one that forms values without parts,
+// 9 more in a backward call, which decides for its two products together.  T = 192, 4096 -> 1024: 75 us on CUDA
+// cores, 31 from parts; T = 512, 512 -> 512: 14 and 17.
+bool parts_pay(int64_t T, int K, int N, bool backward) {
+    if (T <= 16 || T >= ((int64_t)1 << 31) - 1024) return false;
+    const double cores = 7.0 + 2.0 * (double)T * K * N / 27e6;
+    const double split = ((double)T * K + (double)N * K + (backward ? (double)T * N : 0.0)) * 10.0 / 5.5e6 + 8.5;
+    if (!backward) return split + gemm_f32_time(T, N, K, false) < cores;
+    return split + 9.0 + gemm_f32_time(T, K, N, false) + gemm_f32_time(N, K, T, true) < 2.0 * cores;
 }
 
 // Regions of the workspaces, in bytes.  bf16 rows of K elements that are not a multiple of 16 bytes
 // are copied to padded ones (x and W); fp32 operands of the tensor cores are held in parts.
 struct Regions {
-    size_t x, W, dz, part, odd, dzp, total;
+    size_t x, W, dz, part, odd, dzp, tiles, total;
     int64_t ldk, ldn;                  // elements per row of the copies of x and W, and of dz
     bool pad, parts;
 };
@@ -264,7 +271,7 @@ Regions regions(int64_t T, int K, int N, DType dt, bool backward) {
     Regions L{};
     const size_t es = dt == BF16 ? 2 : 4;
     L.pad = dt == BF16 && K % 8 != 0;
-    L.parts = dt == F32 && parts_pay(T, K, N);
+    L.parts = dt == F32 && parts_pay(T, K, N, backward);
     L.ldk = L.pad || L.parts ? padded(K) : K;
     L.ldn = dt == BF16 || L.parts ? padded(N) : N;
     size_t off = 0;
@@ -279,6 +286,11 @@ Regions regions(int64_t T, int K, int N, DType dt, bool backward) {
         L.part = take((size_t)dz_runs(T, N) * N * 4);
         if (L.parts) L.dzp = take((size_t)T * L.ldn * 6);
     }
+    // parts of tiles that the tensor-core kernels share, of one product at a time
+    auto shared = [&](int64_t M, int64_t n, int64_t k, bool a_mn) {
+        return dt == BF16 ? gemm_tc_part_bytes(M, n, k, a_mn) : L.parts ? gemm_f32_part_bytes(M, n, k, a_mn) : 0;
+    };
+    L.tiles = take(backward ? std::max(shared(T, K, N, false), shared(N, K, T, true)) : shared(T, N, K, false));
     L.total = off;
     return L;
 }
@@ -297,6 +309,7 @@ cudaError_t launch_linear(const LinearArgs& a) {
     g.lda = g.ldb = a.K;
     g.M = a.T; g.N = a.N; g.K = a.K;
     g.bias = a.bias; g.residual = a.residual; g.act = a.act; g.D = a.y; g.z = a.z;
+    g.part = reinterpret_cast<float*>(ws + L.tiles);
     g.dt = a.dt; g.stream = a.stream;
     __nv_bfloat16* xc = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
     __nv_bfloat16* wc = reinterpret_cast<__nv_bfloat16*>(ws + L.W);
@@ -353,6 +366,7 @@ cudaError_t launch_linear_backward(const LinearArgs& a) {
     GemmArgs g{};
     g.A = dz ? dz : a.dy;
     g.lda = ldz;
+    g.part = reinterpret_cast<float*>(ws + L.tiles);
     g.dt = a.dt; g.stream = a.stream; g.act = ACT_NONE;
     g.b_mn = true;
     g.ldb = L.pad ? L.ldk : a.K;

@@ -10,7 +10,8 @@
 //     forms 256 x BN tiles with cta_group::2 MMAs (M = 256): each CTA loads its 128 rows of A and
 //     half of B's rows, so a byte of shared memory feeds twice the MMA work of a single CTA's tile.
 //     Persistent: the accumulators are double buffered in TMEM, and the epilogue of one tile runs
-//     under the MMAs of the next.  Warp roles: 0 TMA, 1 MMA issue (first CTA of the pair), 2-17
+//     under the MMAs of the next.  The tiles of the last round, where they leave pairs idle, may be
+//     shared by several pairs along K (Work); join_kernel adds their parts up.  Warp roles: 0 TMA, 1 MMA issue (first CTA of the pair), 2-17
 //     epilogue.
 //   * gemm_split_kernel, for the others (single tokens, small or thin products).  The side with
 //     contiguous output goes on the 128 MMA rows, so a few tokens are a narrow MMA N and a warp's
@@ -52,6 +53,9 @@ constexpr int THREADS = 32 * (2 + EPI);
 constexpr int PAIR_EPI = 16;
 constexpr int CW = 32;                  // columns of outputs that a warp of theirs forms at a time
 constexpr int PAIR_THREADS = 32 * (2 + PAIR_EPI);
+// Clusters that a pair kernel's work is laid out for, one per two SMs of a 148-SM device.  The layout is
+// part of the workspace's size, so it does not follow the device; a smaller one takes more rounds.
+constexpr int PAIRS = 74;
 constexpr unsigned long long kWaitNs = 1000000000ull;    // 1 s per wait
 constexpr unsigned long long kDrainNs = 2000000000ull;   // 2 s for the drains at exit
 constexpr unsigned long long kLandNs = 2000000ull;       // after a failed wait: loads in flight land
@@ -190,9 +194,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// operands, and the outputs D and z of a pair kernel (where their rows are 16-byte aligned)
+// operands, the outputs D and z of a pair kernel (where their rows are 16-byte aligned), and the parts of
+// its shared tiles
 struct Maps {
-    CUtensorMap a, b, d, z;
+    CUtensorMap a, b, d, z, p;
 };
 
 // The wait limit, and the failure-path test hook: stages after which a CTA stops loading (< 0: never)
@@ -303,6 +308,23 @@ __device__ __forceinline__ void finish_block(const Epilogue<T>& ep, const Maps& 
     put(ep.D, maps.d);                   // a lane overwrites its own row of the residual
 }
 
+// A warp's 32 rows x CW columns of a shared tile's part, as they are, in two halves of 64-byte rows
+__device__ __forceinline__ void store_part(const CUtensorMap& map, const float (&v)[CW], unsigned char* out, int c0,
+                                           int64_t r0, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float4*>(out + (lane * 4 + (j ^ ((lane >> 1) & 3))) * 16) =
+                make_float4(v[16 * h + 4 * j], v[16 * h + 4 * j + 1], v[16 * h + 4 * j + 2], v[16 * h + 4 * j + 3]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) tma_store_2d(&map, smem_u32(out), c0 + 16 * h, (int)r0);
+    }
+}
+
 // ------------------------------------------------------------------------- the pair kernel
 
 template <int BN>
@@ -322,6 +344,18 @@ struct PairCfg {
     static_assert(BN / 4 % CW == 0, "whole blocks per epilogue warp");
 };
 
+// What the pairs of a launch do, in this order: tiles 0 .. full - 1 whole, and the others in S parts each
+// along K, which are left in blocks of 256 x BN floats.
+struct Work {
+    int mt, nt, kblocks, S;
+    int64_t full, items;
+};
+
+struct Item {
+    int m, n, k0, k1;
+    int64_t block;                       // of a part, or -1
+};
+
 // Tiles in an order that keeps the operands of those in flight in L2: bands of 8 tile rows, each
 // walked column by column.
 __device__ __forceinline__ void tile_at(int64_t i, int mt, int nt, int& m, int& n) {
@@ -334,10 +368,83 @@ __device__ __forceinline__ void tile_at(int64_t i, int mt, int nt, int& m, int& 
     n = j / rows;
 }
 
+__device__ __forceinline__ Item item_at(int64_t i, const Work& w) {
+    Item it;
+    it.k0 = 0;
+    it.k1 = w.kblocks;
+    it.block = -1;
+    if (i >= w.full) {
+        it.block = i - w.full;
+        const int part = (int)(it.block % w.S);
+        i = w.full + it.block / w.S;
+        it.k0 = (int)((int64_t)w.kblocks * part / w.S);
+        it.k1 = (int)((int64_t)w.kblocks * (part + 1) / w.S);
+    }
+    tile_at(i, w.mt, w.nt, it.m, it.n);
+    return it;
+}
+
+// The outputs of the shared tiles from their parts, added in order: four columns of a row per thread.  The
+// parts were written moments before and come from L2.
+template <typename T, int BN>
+__global__ void __launch_bounds__(256)
+join_kernel(const float* __restrict__ part, const __grid_constant__ Epilogue<T> ep, int64_t M, int64_t N, Work w) {
+    constexpr int ROWS = 256 / (BN / 4);
+    pdl_launch_next();
+    pdl_wait();
+    const int r = blockIdx.x * ROWS + threadIdx.x / (BN / 4), c = threadIdx.x % (BN / 4) * 4;
+    int m, n;
+    tile_at(w.full + blockIdx.y, w.mt, w.nt, m, n);
+    const int64_t row = (int64_t)m * 256 + r, col = (int64_t)n * BN + c;
+    if (row >= M || col >= N) return;
+    const float* p = part + ((int64_t)blockIdx.y * w.S * 256 + r) * BN + c;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < w.S; ++k) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(p + (int64_t)k * 256 * BN));
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+    }
+    const int64_t at = row * N + col;
+    const int left = N - col < 4 ? (int)(N - col) : 4;
+    float res[4] = {0.f, 0.f, 0.f, 0.f};
+    auto put = [&](T* dst) {
+        if (ep.vec) {                    // N is a multiple of four
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<uint2*>(dst + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            else
+                *reinterpret_cast<float4*>(dst + at) = make_float4(v[0], v[1], v[2], v[3]);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < left) store_elem(dst + at + e, v[e]);
+    };
+    if (ep.residual) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < left) res[e] = to_f32(__ldg(ep.residual + at + e));
+    }
+    if (ep.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < left) v[e] += __ldg(ep.bias + col + e);
+    }
+    if (ep.z) put(ep.z);
+    with_act(ep.act, [&](auto kind) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_value<kind(), sizeof(T) == 2>(v[e]);
+    });
+    if (ep.residual) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += res[e];
+    }
+    put(ep.D);
+}
+
 template <int BN, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
-gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<bf16> ep, int64_t M, int64_t N, int kblocks, int mt,
-                 int nt, Limits lim) {
+gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<bf16> ep, int64_t M, int64_t N,
+                 const __grid_constant__ Work work, Limits lim) {
     using C = PairCfg<BN>;
     constexpr int NS = C::NS, KS = C::KS;
     extern __shared__ unsigned char smem_raw[];
@@ -378,22 +485,21 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
     pdl_launch_next();
     pdl_wait();
     const uint32_t tm = tmem_slot;
-    const int64_t tiles = (int64_t)mt * nt;
+    const int64_t items = work.items;
     const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
     if (warp == 0) {
         Ring<NS> ring;
         bool ok = true;
         int left = lim.stop;
-        for (int64_t i = first; ok && left != 0 && i < tiles; i += stride) {
-            int m, n;
-            tile_at(i, mt, nt, m, n);
-            const int m0 = m * 256 + (int)rank * 128, n0 = n * BN + (int)rank * (BN / 2);
-            for (int kb = 0; kb < kblocks && left != 0; kb += KS, ring.next(), --left) {
+        for (int64_t i = first; ok && left != 0 && i < items; i += stride) {
+            const Item it = item_at(i, work);
+            const int m0 = it.m * 256 + (int)rank * 128, n0 = it.n * BN + (int)rank * (BN / 2);
+            for (int kb = it.k0; kb < it.k1 && left != 0; kb += KS, ring.next(), --left) {
                 const int s = ring.s;
                 if (!(ok = wait.warp(empty(s), ring.parity ^ 1u, E_STAGE))) break;
                 if (elect_one()) {
-                    const int nb = kblocks - kb < KS ? kblocks - kb : KS;
+                    const int nb = it.k1 - kb < KS ? it.k1 - kb : KS;
                     if (rank == 0) mbar_arrive_tx(full(s), 2 * C::BLOCK * nb);
                     const uint32_t bar = mapa(full(s), 0);
 #pragma unroll
@@ -430,26 +536,27 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
             Ring<NS> ring;
             int tc = 0;
             bool ok = true;
-            for (int64_t i = first; ok && i < tiles; i += stride, ++tc) {
+            for (int64_t i = first; ok && i < items; i += stride, ++tc) {
+                const Item it = item_at(i, work);
                 const int buf = tc & 1;
                 if (!(ok = wait.warp(acce(buf), ((uint32_t)(tc >> 1) & 1u) ^ 1u, E_ACC))) break;
                 tc_fence_after();
-                for (int kb = 0; kb < kblocks; kb += KS, ring.next()) {
+                for (int kb = it.k0; kb < it.k1; kb += KS, ring.next()) {
                     const int s = ring.s;
                     if (!(ok = wait.warp(full(s), ring.parity, E_STAGE))) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int u = 0; u < KS; ++u) {
-                            if (kb + u >= kblocks) break;
+                            if (kb + u >= it.k1) break;
                             const uint32_t off = (uint32_t)(s * (C::STAGE >> 4) + u * (C::BLOCK >> 4));
 #pragma unroll
                             for (int k = 0; k < BK / 16; ++k)
                                 mma_pair(tm + buf * BN, da0 + off + k * K16<A_MN>, db0 + off + k * K16<B_MN>, ID,
-                                         (kb > 0 || u > 0 || k > 0) ? 1u : 0u);
+                                         (kb > it.k0 || u > 0 || k > 0) ? 1u : 0u);
                         }
                         mma_commit_pair(empty(s));
-                        if (kb + KS >= kblocks) mma_commit_pair(accf(buf));
+                        if (kb + KS >= it.k1) mma_commit_pair(accf(buf));
                     }
                     __syncwarp();
                 }
@@ -470,12 +577,11 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
         unsigned char* out = sm + NS * C::STAGE + (warp - 2) * 32 * CW * 2;
         const uint32_t acce_first[2] = {mapa(acce(0), 0), mapa(acce(1), 0)};
         int tc = 0;
-        for (int64_t i = first; i < tiles; i += stride, ++tc) {
+        for (int64_t i = first; i < items; i += stride, ++tc) {
             const int buf = tc & 1;
-            int m, n;
-            tile_at(i, mt, nt, m, n);
-            const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q, c0 = (int64_t)n * BN + h * (BN / 4);
-            prefetch_residual(ep, r0, c0, BN / 4, M, N, lane);
+            const Item it = item_at(i, work);
+            const int64_t r0 = (int64_t)it.m * 256 + rank * 128 + 32 * q, c0 = (int64_t)it.n * BN + h * (BN / 4);
+            if (it.block < 0) prefetch_residual(ep, r0, c0, BN / 4, M, N, lane);
             if (!wait.warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC)) break;
             tc_fence_after();
 #pragma unroll 1
@@ -483,7 +589,10 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
                 if (c0 + c >= N || r0 >= M) continue;
                 float v[CW];
                 tmem_ld32(tq + buf * BN + c, v);
-                finish_block<bf16>(ep, maps, v, out, r0, c0 + c, M, N, lane);
+                if (it.block < 0)
+                    finish_block<bf16>(ep, maps, v, out, r0, c0 + c, M, N, lane);
+                else
+                    store_part(maps.p, v, out, h * (BN / 4) + c, it.block * 256 + rank * 128 + 32 * q, lane);
             }
             tc_fence_before();
             __syncwarp();
@@ -529,7 +638,7 @@ struct F32Cfg {
 template <bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<float> ep, int64_t M, int64_t N,
-                int kblocks, int mt, int nt, Limits lim) {
+                const __grid_constant__ Work work, Limits lim) {
     using C = F32Cfg;
     constexpr int NS = C::NS, BN = C::BN;
     extern __shared__ unsigned char smem_raw[];
@@ -568,18 +677,17 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
     pdl_launch_next();                   // as in the pair kernel
     pdl_wait();
     const uint32_t tm = tmem_slot;
-    const int64_t tiles = (int64_t)mt * nt;
+    const int64_t items = work.items;
     const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
     if (warp == 0) {
         Ring<NS> ring;
         bool ok = true;
         int left = lim.stop;
-        for (int64_t i = first; ok && left != 0 && i < tiles; i += stride) {
-            int m, n;
-            tile_at(i, mt, nt, m, n);
-            const int m0 = m * 256 + (int)rank * 128, n0 = n * BN + (int)rank * (BN / 2);
-            for (int kb = 0; kb < kblocks && left != 0; ++kb, ring.next(), --left) {
+        for (int64_t i = first; ok && left != 0 && i < items; i += stride) {
+            const Item it = item_at(i, work);
+            const int m0 = it.m * 256 + (int)rank * 128, n0 = it.n * BN + (int)rank * (BN / 2);
+            for (int kb = it.k0; kb < it.k1 && left != 0; ++kb, ring.next(), --left) {
                 const int s = ring.s;
                 if (!(ok = wait.warp(empty(s), ring.parity ^ 1u, E_STAGE))) break;
                 if (elect_one()) {
@@ -616,12 +724,13 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
             Ring<NS> ring;
             int tc = 0;
             bool ok = true;
-            for (int64_t i = first; ok && i < tiles; i += stride) {
-                for (int kb = 0; ok && kb < kblocks; ++tc) {
+            for (int64_t i = first; ok && i < items; i += stride) {
+                const Item it = item_at(i, work);
+                for (int kb = it.k0; ok && kb < it.k1; ++tc) {
                     const int buf = tc & 1;
                     if (!(ok = wait.warp(acce(buf), ((uint32_t)(tc >> 1) & 1u) ^ 1u, E_ACC))) break;
                     tc_fence_after();
-                    const int end = kb + C::CHUNK < kblocks ? kb + C::CHUNK : kblocks;
+                    const int end = kb + C::CHUNK < it.k1 ? kb + C::CHUNK : it.k1;
                     for (bool fresh = true; kb < end; ++kb, fresh = false, ring.next()) {
                         const int s = ring.s;
                         if (!(ok = wait.warp(full(s), ring.parity, E_STAGE))) break;
@@ -657,13 +766,12 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
         const uint32_t acce_first[2] = {mapa(acce(0), 0), mapa(acce(1), 0)};
         int tc = 0;
         bool ok = true;
-        for (int64_t i = first; ok && i < tiles; i += stride) {
-            int m, n;
-            tile_at(i, mt, nt, m, n);
-            const int64_t r0 = (int64_t)m * 256 + rank * 128 + 32 * q, c0 = (int64_t)n * BN + h * CW;
-            prefetch_residual(ep, r0, c0, CW, M, N, lane);
+        for (int64_t i = first; ok && i < items; i += stride) {
+            const Item it = item_at(i, work);
+            const int64_t r0 = (int64_t)it.m * 256 + rank * 128 + 32 * q, c0 = (int64_t)it.n * BN + h * CW;
+            if (it.block < 0) prefetch_residual(ep, r0, c0, CW, M, N, lane);
             float sum[CW] = {};
-            for (int kb = 0; kb < kblocks; kb += C::CHUNK, ++tc) {
+            for (int kb = it.k0; kb < it.k1; kb += C::CHUNK, ++tc) {
                 const int buf = tc & 1;
                 if (!(ok = wait.warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC))) break;
                 tc_fence_after();
@@ -677,7 +785,11 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
                 if (lane == 0) arrive_cluster(buf ? acce_first[1] : acce_first[0]);
             }
             if (!ok) break;
-            if (c0 < N && r0 < M) finish_block<float>(ep, maps, sum, out, r0, c0, M, N, lane);
+            if (c0 >= N || r0 >= M) continue;
+            if (it.block < 0)
+                finish_block<float>(ep, maps, sum, out, r0, c0, M, N, lane);
+            else
+                store_part(maps.p, sum, out, h * CW, it.block * 256 + rank * 128 + 32 * q, lane);
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
@@ -997,47 +1109,70 @@ Epilogue<T> epilogue_of(const GemmArgs& g) {
     return ep;
 }
 
-template <int BN, bool A_MN, bool B_MN>
-cudaError_t pair_launch(const GemmArgs& g, int sms) {
-    using C = PairCfg<BN>;
-    auto kern = gemm_pair_kernel<BN, A_MN, B_MN>;
-    cudaError_t e = allow_smem(kern, C::SMEM);
+// The blocks of 256 x BN floats that hold the parts of shared tiles, stored in boxes of 32 x 16
+bool make_map_parts(CUtensorMap* map, void* p, int64_t blocks, int bn) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)bn, (cuuint64_t)(256 * blocks)};
+    const cuuint64_t str[1] = {(cuuint64_t)bn * 4};
+    const cuuint32_t box[2] = {16, 32};
+    const cuuint32_t e1[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p, dims, str, box, e1, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+Work work_of(int64_t M, int64_t N, int64_t K, int bn, int S) {
+    Work w{};
+    w.mt = (int)((M + 255) / 256);
+    w.nt = (int)((N + bn - 1) / bn);
+    w.kblocks = (int)((K + BK - 1) / BK);
+    w.S = S;
+    const int64_t tiles = (int64_t)w.mt * w.nt;
+    w.full = S > 1 ? tiles / PAIRS * PAIRS : tiles;
+    w.items = w.full + (tiles - w.full) * S;
+    return w;
+}
+
+// The pair kernel on its work, and the sums of the shared tiles after it
+template <typename T, int BN, typename K>
+cudaError_t launch_pairs(K kern, int smem, Maps& maps, const GemmArgs& g, int S, int sms) {
+    cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    Maps maps{};
-    const Epilogue<bf16> ep = epilogue_of<bf16>(g);
-    if (!make_map(&maps.a, g.A, g.M, g.K, g.lda, A_MN, 128) || !make_map(&maps.b, g.B, g.N, g.K, g.ldb, B_MN, BN / 2) ||
-        !output_maps(&maps, ep, g.M, g.N))
+    const Epilogue<T> ep = epilogue_of<T>(g);
+    const Work w = work_of(g.M, g.N, g.K, BN, S);
+    const int64_t shared = w.items - w.full, pairs = sms / 2;
+    if (!output_maps(&maps, ep, g.M, g.N) || (shared && !make_map_parts(&maps.p, g.part, shared, BN)))
         return cudaErrorInvalidValue;
-    const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + BN - 1) / BN);
-    const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
-    const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)C::SMEM, g.stream, maps, ep, g.M, g.N,
-                      (int)((g.K + BK - 1) / BK), mt, nt, limits());
+    const unsigned grid = 2u * (unsigned)(w.items < pairs ? w.items : pairs);
+    e = launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)smem, g.stream, maps, ep, g.M, g.N, w, limits());
+    if (e != cudaSuccess || !shared) return e;
+    return launch_pdl(join_kernel<T, BN>, dim3(BN / 4, (unsigned)(shared / S)), dim3(256), 0, g.stream,
+                      static_cast<const float*>(g.part), ep, g.M, g.N, w);
+}
+
+template <int BN, bool A_MN, bool B_MN>
+cudaError_t pair_launch(const GemmArgs& g, int S, int sms) {
+    Maps maps{};
+    if (!make_map(&maps.a, g.A, g.M, g.K, g.lda, A_MN, 128) || !make_map(&maps.b, g.B, g.N, g.K, g.ldb, B_MN, BN / 2))
+        return cudaErrorInvalidValue;
+    return launch_pairs<bf16, BN>(gemm_pair_kernel<BN, A_MN, B_MN>, PairCfg<BN>::SMEM, maps, g, S, sms);
 }
 
 template <int BN>
-cudaError_t pair_layout(const GemmArgs& g, int sms) {
-    if (g.a_mn) return g.b_mn ? pair_launch<BN, true, true>(g, sms) : cudaErrorInvalidValue;
-    return g.b_mn ? pair_launch<BN, false, true>(g, sms) : pair_launch<BN, false, false>(g, sms);
+cudaError_t pair_layout(const GemmArgs& g, int S, int sms) {
+    if (g.a_mn) return g.b_mn ? pair_launch<BN, true, true>(g, S, sms) : cudaErrorInvalidValue;
+    return g.b_mn ? pair_launch<BN, false, true>(g, S, sms) : pair_launch<BN, false, false>(g, S, sms);
 }
 
 template <bool A_MN, bool B_MN>
-cudaError_t f32_launch(const GemmArgs& g, const F32Planes& f, int sms) {
-    using C = F32Cfg;
-    auto kern = gemm_f32_kernel<A_MN, B_MN>;
-    cudaError_t e = allow_smem(kern, C::SMEM);
-    if (e != cudaSuccess) return e;
+cudaError_t f32_launch(const GemmArgs& g, const F32Planes& f, int S, int sms) {
+    constexpr int BN = F32Cfg::BN;
     Maps maps{};
-    const Epilogue<float> ep = epilogue_of<float>(g);
     if (!make_map_planes(&maps.a, f.A, g.M, g.K, f.lda, f.a_plane, A_MN, 128) ||
-        !make_map_planes(&maps.b, f.B, g.N, g.K, f.ldb, f.b_plane, B_MN, C::BN / 2) ||
-        !output_maps(&maps, ep, g.M, g.N))
+        !make_map_planes(&maps.b, f.B, g.N, g.K, f.ldb, f.b_plane, B_MN, BN / 2))
         return cudaErrorInvalidValue;
-    const int mt = (int)((g.M + 255) / 256), nt = (int)((g.N + C::BN - 1) / C::BN);
-    const int64_t tiles = (int64_t)mt * nt, pairs = sms / 2;
-    const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)C::SMEM, g.stream, maps, ep, g.M, g.N,
-                      (int)((g.K + BK - 1) / BK), mt, nt, limits());
+    return launch_pairs<float, BN>(gemm_f32_kernel<A_MN, B_MN>, F32Cfg::SMEM, maps, g, S, sms);
 }
 
 template <int BN, bool A_MN, bool B_MN>
@@ -1091,8 +1226,33 @@ namespace {
 // Which kernel runs a product.
 struct Plan {
     int pair_bn;                         // 256 or 128: the pair kernel; 0: the split kernel
-    int bn, S;                           // of the split kernel
+    int bn, S;                           // of the split kernel; S: clusters per tile, of the pair kernel's last round
 };
+
+constexpr int SMS = 2 * lintc::PAIRS;
+
+// The time, in us, of a pair kernel whose K blocks take `per_kb` each and whose tiles at least `least`, and the
+// best number S of pairs for a tile of its last round.  Sharing takes a second kernel (3 us) and the traffic of
+// the parts (rem S blocks of bn x 1 KB).  A shared tile adds up K in another order than a whole one, so a product
+// whose rows are tokens shares all its tiles or none: equal tokens of a call get equal bits.  (a_mn: rows are
+// channels.)
+double pair_time(int64_t M, int64_t N, int64_t K, bool a_mn, int bn, double per_kb, double least, int* S) {
+    const int64_t kb = (K + 63) / 64, tiles = ((M + 255) / 256) * ((N + bn - 1) / bn);
+    const int64_t full = tiles / lintc::PAIRS, rem = tiles % lintc::PAIRS;
+    const double tile = std::max(per_kb * kb, least);
+    *S = 1;
+    if (!rem) return full * tile;
+    if (full && !a_mn) return (full + 1) * tile;
+    double last = tile;
+    for (int s = 2; s <= 16 && rem * s <= lintc::PAIRS && kb >= 4 * s; ++s) {
+        const double t = std::max(per_kb * ((kb + s - 1) / s), least) + 3.0 + 0.06 * rem * s * bn / 256;
+        if (t < last) {
+            last = t;
+            *S = s;
+        }
+    }
+    return full * tile + last;
+}
 
 // Up to 64 rows of A, the split kernel with the narrowest MMA N that holds them, and K split until two
 // CTAs per SM stream the other operand.  Above that, the smallest of these times, in us, with kb
@@ -1102,30 +1262,32 @@ struct Plan {
 //   pair, 256 x 128   w max(0.185 kb, 2.0)     8.0 at T = 512, 1024 -> 1024 (256 x 256: 11, split: 9.4)
 //   split by S        w (0.23 kb / S + 3.5) - 3, and 3 more to join the parts
 //                                              17 at T = 333, 8192 -> 1000 with S = 4 (pair: 29)
-Plan plan(const GemmArgs& g, int sms) {
+Plan plan(int64_t M, int64_t N, int64_t K, bool a_mn) {
     Plan p{};
-    const int64_t kb = (g.K + 63) / 64, rows = (g.N + 127) / 128;
+    const int64_t kb = (K + 63) / 64, rows = (N + 127) / 128;
     auto rounds = [](int64_t tiles, int64_t at_once) { return (double)((tiles + at_once - 1) / at_once); };
-    if (g.M <= 64) {
-        p.bn = g.a_mn || g.M > 32 ? 64 : g.M > 16 ? 32 : 16;    // a product over tokens has boxes of 64
+    if (M <= 64) {
+        p.bn = a_mn || M > 32 ? 64 : M > 16 ? 32 : 16;    // a product over tokens has boxes of 64
         const int64_t tiles = rows;
         p.S = 1;
-        while (p.S < 8 && tiles * p.S * 2 <= 2 * sms && kb >= p.S * 4) p.S *= 2;
+        while (p.S < 8 && tiles * p.S * 2 <= 2 * SMS && kb >= p.S * 4) p.S *= 2;
         return p;
     }
-    const int64_t mt = (g.M + 255) / 256;
-    double best = rounds(mt * ((g.N + 255) / 256), sms / 2) * std::max(0.30 * kb, 2.9);
+    int s256, s128;
+    double best = pair_time(M, N, K, a_mn, 256, 0.30, 2.9, &s256);
+    const double half = pair_time(M, N, K, a_mn, 128, 0.185, 2.0, &s128);
     p.pair_bn = 256;
-    const double half = rounds(mt * ((g.N + 127) / 128), sms / 2) * std::max(0.185 * kb, 2.0);
+    p.S = s256;
     if (half < best) {
         best = half;
         p.pair_bn = 128;
+        p.S = s128;
     }
     p.bn = 128;
     for (int S = 1; S <= 8 && kb >= 2 * S - 1; S *= 2) {
         // clusters at once: a GPC of 16 to 20 SMs holds two clusters of 8
-        const int64_t at_once = S == 8 ? sms * 3 / 32 : sms / S;
-        const double t = rounds(rows * ((g.M + 127) / 128), at_once) * (0.23 * kb / S + 3.5 + (S > 1 ? 3.0 : 0.0)) - 3.0;
+        const int64_t at_once = S == 8 ? SMS * 3 / 32 : SMS / S;
+        const double t = rounds(rows * ((M + 127) / 128), at_once) * (0.23 * kb / S + 3.5 + (S > 1 ? 3.0 : 0.0)) - 3.0;
         if (t < best) {
             best = t;
             p.pair_bn = 0;
@@ -1135,15 +1297,40 @@ Plan plan(const GemmArgs& g, int sms) {
     return p;
 }
 
+double f32_time(int64_t M, int64_t N, int64_t K, bool a_mn, int* S) {
+    return pair_time(M, N, K, a_mn, lintc::F32Cfg::BN, 1.1, 4.0, S);
+}
+
+size_t part_bytes(int64_t M, int64_t N, int64_t K, int bn, int S) {
+    const lintc::Work w = lintc::work_of(M, N, K, bn, S);
+    return (size_t)(w.items - w.full) * 256 * bn * 4;
+}
+
 }  // namespace
+
+size_t gemm_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool a_mn) {
+    const Plan p = plan(M, N, K, a_mn);
+    return p.pair_bn ? part_bytes(M, N, K, p.pair_bn, p.S) : 0;
+}
+
+size_t gemm_f32_part_bytes(int64_t M, int64_t N, int64_t K, bool a_mn) {
+    int S;
+    f32_time(M, N, K, a_mn, &S);
+    return part_bytes(M, N, K, lintc::F32Cfg::BN, S);
+}
+
+double gemm_f32_time(int64_t M, int64_t N, int64_t K, bool a_mn) {
+    int S;
+    return f32_time(M, N, K, a_mn, &S);
+}
 
 cudaError_t launch_gemm_tc(const GemmArgs& g) {
     DeviceInfo di;
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
-    const Plan p = plan(g, di.sm_count);
-    if (p.pair_bn == 256) return lintc::pair_layout<256>(g, di.sm_count);
-    if (p.pair_bn == 128) return lintc::pair_layout<128>(g, di.sm_count);
+    const Plan p = plan(g.M, g.N, g.K, g.a_mn);
+    if (p.pair_bn == 256) return lintc::pair_layout<256>(g, p.S, di.sm_count);
+    if (p.pair_bn == 128) return lintc::pair_layout<128>(g, p.S, di.sm_count);
     switch (p.bn) {
         case 16: return lintc::split_layout<16>(g, p.S);
         case 32: return lintc::split_layout<32>(g, p.S);
@@ -1156,9 +1343,11 @@ cudaError_t launch_gemm_f32(const GemmArgs& g, const F32Planes& f) {
     DeviceInfo di;
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
-    if (g.a_mn) return g.b_mn ? lintc::f32_launch<true, true>(g, f, di.sm_count) : cudaErrorInvalidValue;
-    return g.b_mn ? lintc::f32_launch<false, true>(g, f, di.sm_count)
-                  : lintc::f32_launch<false, false>(g, f, di.sm_count);
+    int S;
+    f32_time(g.M, g.N, g.K, g.a_mn, &S);
+    if (g.a_mn) return g.b_mn ? lintc::f32_launch<true, true>(g, f, S, di.sm_count) : cudaErrorInvalidValue;
+    return g.b_mn ? lintc::f32_launch<false, true>(g, f, S, di.sm_count)
+                  : lintc::f32_launch<false, false>(g, f, S, di.sm_count);
 }
 
 void linear_tc_set_stop(int stop, unsigned long long wait_ns) {
