@@ -1418,6 +1418,16 @@ std::atomic<int> g_stop{-1};
 
 Limits limits() { return Limits{g_wait_ns.load(), g_stop.load()}; }
 
+// Shared memory of an SM that the blocks of a ring kernel split among them
+constexpr int ROOM = 204800;
+
+// The same limit at every launch, whatever the launch takes of it: another host thread may be launching the
+// kernel for other rows.
+template <typename K>
+cudaError_t allow_room(K kern) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ROOM);
+}
+
 // Launch shape of a ring kernel: threads, rows per slot, and slots.  The SM's shared memory goes to
 // about 640 threads' worth of blocks.
 struct RingShape {
@@ -1433,7 +1443,7 @@ RingShape ring_shape(int d, int nv, int r, int g, int tensors) {
     s.threads = consumers + 32;
     s.B = g ? WARPS * (32 / g) * r : r;
     const size_t slot = (size_t)tensors * s.B * d * sizeof(T);
-    s.slots = (int)(204800 / blocks / slot);
+    s.slots = (int)(ROOM / blocks / slot);
     s.slots = s.slots < 2 ? 2 : s.slots > MAX_SLOTS ? MAX_SLOTS : s.slots;
     s.bytes = s.slots * slot;
     return s;
@@ -1443,7 +1453,7 @@ template <typename T, int NV, int R, int G, int TH>
 cudaError_t fwd_ring(const LnArgs& a) {
     const RingShape r = ring_shape<T>(a.d, NV, R, G, 1);
     auto kern = ln_fwd_ring_kernel<T, NV, R, G, TH>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)r.bytes);
+    cudaError_t e = allow_room(kern);
     if (e != cudaSuccess) return e;
     const int64_t want = (a.T + r.B - 1) / r.B;
     int cap;
@@ -1458,7 +1468,7 @@ template <typename T, int NV, int R, int G, int TH>
 cudaError_t bwd_ring(const LnArgs& a, int* blocks) {
     const RingShape r = ring_shape<T>(a.d, NV, R, G, 2);
     auto kern = ln_bwd_ring_kernel<T, NV, R, G, TH>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)r.bytes);
+    cudaError_t e = allow_room(kern);
     if (e != cudaSuccess) return e;
     // four rows per block at least: a block's column sums cost as much traffic as its first two rows
     const int64_t batches = (a.T + r.B - 1) / r.B, want = r.B >= 4 ? batches : (batches * r.B + 3) / 4;
@@ -1478,10 +1488,10 @@ cudaError_t fwd_warp(const LnArgs& a) {
     auto kern = ln_fwd_warp_kernel<T, NV>;
     // the SM's shared memory in equal parts
     const size_t wb = (size_t)2 * NV * 32 * Vec16<T>::VEC * 4, slot = (size_t)(TH / 32) * a.d * sizeof(T);
-    int slots = (int)((204800 / WARP_BLOCKS<NV> - wb) / slot);
+    int slots = (int)((ROOM / WARP_BLOCKS<NV> - wb) / slot);
     slots = slots < 1 ? 1 : slots > WARP_SLOTS ? WARP_SLOTS : slots;
     const size_t smem = wb + slots * slot;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_room(kern);
     if (e != cudaSuccess) return e;
     const int64_t want = (a.T + TH / 32 - 1) / (TH / 32);
     int cap;
@@ -1498,10 +1508,10 @@ cudaError_t fwd_shift(const LnArgs& a) {
     auto kern = ln_fwd_shift_kernel<T, NV>;
     const size_t wb = (size_t)2 * NV * 32 * Vec16<T>::VEC * 4;
     const size_t slot = (size_t)(TH / 32) * ((a.d * sizeof(T) + 15) / 16 * 16 + 16);
-    int slots = (int)((204800 / WARP_BLOCKS<NV> - wb) / slot);
+    int slots = (int)((ROOM / WARP_BLOCKS<NV> - wb) / slot);
     slots = slots < 1 ? 1 : slots > WARP_SLOTS ? WARP_SLOTS : slots;
     const size_t smem = wb + slots * slot;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_room(kern);
     if (e != cudaSuccess) return e;
     const int64_t want = (a.T + TH / 32 - 1) / (TH / 32);
     int cap;
@@ -1519,9 +1529,9 @@ cudaError_t bwd_shift(const LnArgs& a, int* blocks) {
     auto kern = ln_bwd_shift_kernel<T, NV, R, TH>;
     const int words = (a.d + 2 * VEC - 2) / VEC, nthr = ((words + NV - 1) / NV + 31) / 32 * 32;
     const size_t slot = (size_t)2 * R * ((a.d * sizeof(T) + 15) / 16 * 16 + 16);
-    int slots = (int)(204800 / (nthr >= 320 ? 2 : nthr <= 64 ? 10 : 640 / nthr) / slot);
+    int slots = (int)(ROOM / (nthr >= 320 ? 2 : nthr <= 64 ? 10 : 640 / nthr) / slot);
     slots = slots < 2 ? 2 : slots > MAX_SLOTS ? MAX_SLOTS : slots;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(slots * slot));
+    cudaError_t e = allow_room(kern);
     if (e != cudaSuccess) return e;
     const int64_t want = (a.T + 3) / 4;
     int cap;
@@ -1535,8 +1545,12 @@ cudaError_t bwd_shift(const LnArgs& a, int* blocks) {
 }
 
 // The layout of a row by its length in vectors: 8, 16 or 32 lanes with one vector each, 32 with two, a
-// warp with up to 16, a block with two (then four) per thread.  At most one row per SM takes a register
-// kernel.
+// warp with up to 16, a block with more.  What a block's row costs is the time between its load and its
+// store, which other warps have to cover: several small blocks per SM, or one of ten warps and more whose
+// threads hold few registers each.  Measured, us: bf16, T = 8192, d = 6000, 4 vectors per thread and one row
+// 53 (2 and two rows: 59; 6: 53), d = 8192, 4 and two rows 66 (2 and two: 70, 4 and one: 76); fp32, T = 8192,
+// d = 7400, 6 and two rows 84 (4 and one: 107, 8 and one: 90), d = 5000, T = 5052, 8 and one 39 (42, 42).  At
+// most one row per SM takes a register kernel.
 // Rows that are not a multiple of 16 bytes take the shift kernels from 16 rows per SM on.  T = 16384,
 // bf16: d = 4095 forward 68 us against 132 one element at a time, backward 123 against 165; d = 2559
 // backward 86 against 104.  With fewer rows filling the ring costs more than it hides: T = 1200, d = 1037
@@ -1558,18 +1572,23 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
         if (c <= 320) return fwd_warp<T, 10>(a);
         if (c <= 384) return fwd_warp<T, 12>(a);
         if (c <= 512) return fwd_warp<T, 16>(a);
-        if (c <= 1024) return fwd_ring<T, 2, 2, 0, 512>(a);
+        if (V == 8 && c <= 896) return fwd_ring<T, 4, 1, 0, 256>(a);
+        if (c <= 1024) return fwd_ring<T, 4, 2, 0, 256>(a);
+        if (V == 4 && c <= 1280) return fwd_ring<T, 8, 1, 0, 256>(a);
+        if (V == 4 && c <= 2048) return fwd_ring<T, 6, 2, 0, 352>(a);
         if (c <= 2048) return fwd_ring<T, 4, 1, 0, 512>(a);
     } else {
         // vectors that the words around a row may take
         const int c = ((int)sizeof(T) * a.d + 30) / 16;
-        if (a.T >= 16 * sms && a.d > 256 && c <= 544 && rows16(a.x) && rows16(a.y)) {
+        if (a.T >= 16 * sms && a.d > 256 && c <= 1026 && rows16(a.x) && rows16(a.y)) {
             if (c <= 128) return fwd_shift<T, 4>(a);
             if (c <= 192) return fwd_shift<T, 6>(a);
             if (c <= 256) return fwd_shift<T, 8>(a);
             if (c <= 320) return fwd_shift<T, 10>(a);
             if (c <= 384) return fwd_shift<T, 12>(a);
-            return fwd_shift<T, 17>(a);
+            if (c <= 544) return fwd_shift<T, 17>(a);
+            if (c <= 768) return fwd_shift<T, 24>(a);
+            return fwd_shift<T, 33>(a);          // eight rows and the columns' w and b fill the SM's shared memory
         }
         if (a.d <= 256) return fwd<T, 1, 8, 2, true>(a);
         if (a.d <= 4096) return fwd<T, 1, 8, 2, false>(a);
@@ -1582,10 +1601,11 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
                       static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
 }
 
-// As forward, but a block has two vectors per thread and two rows at a time.  320 to 480 vectors: three
-// and one, because two need six warps or more, whose registers leave room for one block per SM only (T =
-// 16384, bf16, d = 2816: 60 us against 79, d = 3584: 71 against 80; d = 4096 needs six warps either way:
-// 77 with two, 115 with three).
+// As forward, but a block has two vectors per thread and two rows at a time up to 512 vectors, and three
+// (fp32, above 1024: six) and one above (T = 8192, bf16, d = 8192: 83 us, 142 with two; fp32 97, 172 with
+// four; odd widths, d = 6001: 101, 132 with two).  320 to 480 vectors: three and one, because two need six
+// warps or more, whose registers leave room for one block per SM only (T = 16384, bf16, d = 2816: 60 us
+// against 79, d = 3584: 71 against 80; d = 4096 needs six warps either way: 77 with two, 115 with three).
 template <typename T>
 cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
     constexpr int V = Vec16<T>::VEC;
@@ -1599,16 +1619,16 @@ cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
         if (c <= 64) return bwd_ring<T, 2, 1, 32, W>(a, blocks);
         if (c > 320 && c <= 480) return bwd_ring<T, 3, 1, 0, 256>(a, blocks);
         if (c <= 512) return bwd_ring<T, 2, 2, 0, 256>(a, blocks);
-        if (c <= 1024) return bwd_ring<T, 2, 1, 0, 512>(a, blocks);
+        if (c <= 1024) return bwd_ring<T, 3, 1, 0, 352>(a, blocks);
         if constexpr (V == 4) {
-            if (c <= 2048) return bwd_ring<T, 4, 1, 0, 512>(a, blocks);
+            if (c <= 2048) return bwd_ring<T, 6, 1, 0, 352>(a, blocks);
         }
     } else {
         const int c = ((int)sizeof(T) * a.d + 30) / 16;
         if (a.T >= 16 * sms && a.d > 256 && c <= 1024 && rows16(a.x) && rows16(a.dy) && rows16(a.dx)) {
             if (c > 320 && c <= 480) return bwd_shift<T, 3, 1, 256>(a, blocks);
             if (c <= 512) return bwd_shift<T, 2, 2, 256>(a, blocks);
-            return bwd_shift<T, 2, 1, 512>(a, blocks);
+            return bwd_shift<T, 3, 1, 352>(a, blocks);
         }
         if (a.d <= 256) return bwd<T, 1, 8, 1, true>(a, blocks);
         if (a.d <= 4096) return bwd<T, 1, 8, 1, false>(a, blocks);

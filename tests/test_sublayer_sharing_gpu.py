@@ -215,3 +215,37 @@ def test_linear_past_32_bit_offsets(N):
     n[:T - last] += 1
     check(db, (n @ dz).cpu(), (n @ e0 + (T + 80) * U * (n @ dz.abs())).cpu(), "dbias")
     assert mhc.mhc_device_status() == 0
+
+
+def test_two_host_threads_at_once():
+    # rows of many lengths that share kernels, each thread on a stream of its own
+    import threading
+    errors = []
+    widths = ([2048, 1544, 2560, 4096, 520], [1800, 2048, 4000, 2112, 600])
+
+    def work(k):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                layers = [_Layer(600, d, 136, BF, seed=d) for d in widths[k]]
+                s.synchronize()
+                for _ in range(2):
+                    for _ in range(30):
+                        for m in layers:
+                            m.run()
+                    s.synchronize()
+                    res = [[t.clone() for t in m.outputs()] for m in layers]
+                    for m, ref in zip(layers, res):
+                        m.run()
+                        s.synchronize()
+                        assert all(torch.equal(p, q) for p, q in zip(m.outputs(), ref))
+        except BaseException as e:      # noqa: BLE001 -- reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert mhc.mhc_device_status() == 0
