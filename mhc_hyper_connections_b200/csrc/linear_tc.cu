@@ -11,8 +11,8 @@
 //     half of B's rows, so a byte of shared memory feeds twice the MMA work of a single CTA's tile.
 //     Persistent: the accumulators are double buffered in TMEM, and the epilogue of one tile runs
 //     under the MMAs of the next.  The tiles of the last round, where they leave pairs idle, may be
-//     shared by several pairs along K (Work); join_kernel adds their parts up.  Warp roles: 0 TMA, 1 MMA issue (first CTA of the pair), 2-17
-//     epilogue.
+//     shared by several pairs along K (Work); join_kernel adds their parts up (T = 700, 8192 -> 1100:
+//     15 tiles in 4 parts each).  Warp roles: 0 TMA, 1 MMA issue (first CTA of the pair), 2-17 epilogue.
 //   * gemm_split_kernel, for the others (single tokens, small or thin products).  The side with
 //     contiguous output goes on the 128 MMA rows, so a few tokens are a narrow MMA N and a warp's
 //     stores are contiguous.  A cluster of S CTAs shares a tile by splitting K; the partial tiles
