@@ -935,9 +935,6 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
             drain.warp(drained, 0u, E_DRAIN, false);
         }
         __syncwarp();
-    } else {
-        done = wait.warp(accf, 0u, E_ACC);
-        tc_fence_after();
     }
 
     const int q = warp & 3, h = (warp - 2) >> 2;
@@ -945,13 +942,26 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
     const uint32_t tq = tm + ((uint32_t)(32 * q) << 16);
     const float bias = warp >= 2 && ep.bias && r < Mr ? __ldg(ep.bias + r) : 0.f;
     constexpr int HALF = BN / 2;
+    // a whole tile's residual, on its way while the sums are formed
+    bf16 res[HALF];
+    if (warp >= 2) {
+        if (S == 1 && ep.residual) {
+#pragma unroll
+            for (int c = 0; c < HALF; ++c)
+                if (n0 + h * HALF + c < Nc && r < Mr) res[c] = __ldg(ep.residual + (n0 + (int64_t)h * HALF + c) * Mr + r);
+        }
+        done = wait.warp(accf, 0u, E_ACC);
+        tc_fence_after();
+    }
     if (S == 1) {
         // a thread owns a row; its stores and those of its warp's other lanes are contiguous
         if (warp >= 2 && done) {
             const int c_lo = h * HALF, c_hi = c_lo + HALF < Nc - n0 ? c_lo + HALF : (int)(Nc - n0);
             with_act(ep.act, [&](auto kind) {
-#pragma unroll 1
-                for (int c = c_lo; c < c_hi; c += 8) {
+#pragma unroll
+                for (int i = 0; i < HALF; i += 8) {
+                    const int c = c_lo + i;
+                    if (c >= c_hi) break;
                     float v[8];
                     tmem_ld8(tq + c, v);
                     int64_t at = (n0 + (int64_t)c) * Mr + r;
@@ -961,7 +971,7 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
                             const float z = v[j] + bias;
                             if (ep.z) store_elem(ep.z + at, z);
                             float o = act_value<kind(), true>(z);
-                            if (ep.residual) o += to_f32(__ldg(ep.residual + at));
+                            if (ep.residual) o += to_f32(res[i + j]);
                             store_elem(ep.D + at, o);
                         }
                 }
