@@ -24,7 +24,7 @@
 //   * long kernels, for rows beyond the registers of a block: three walks over the row.
 // Column sums are added up in a fixed order: over a group's rows, over a block's warps in shared
 // memory, and over the blocks by a second kernel that reads one fp32 row pair per block; or, for few
-// rows, by a kernel that reads the rows once more beside the first one.
+// rows, by a kernel that reads the rows once more beside the first one, or by blocks of the same launch.
 #include <atomic>
 
 #include "common.cuh"
@@ -45,6 +45,10 @@ int bwd_blocks(int d) { return d >= 4096 ? 296 : d <= 1024 ? 1184 : 296 * 4096 /
 // kernel runs; above it from the row kernel's registers through `part`.  d = 2560, bf16, T = 128: 3.5 us
 // against 8.2, T = 500: 6.4 against 9.6, T = 1000: 14.4 against 11.5.
 constexpr int FEW_ROWS = 512;
+// Up to here both are one launch, where a block holds a row with one vector per thread: a call 9.7 us against
+// 12.1 (bound by the host; in a graph, bf16, T = 200, d = 1024: 3.6 against 3.7, T = 256, d = 4096: 5.9 and 6.6,
+// unaligned d = 515: 4.9 and 3.6).  Its column blocks have half the warps, so many rows take them longer.
+constexpr int ONE_LAUNCH_ROWS = 256;
 constexpr int WARPS = 8;               // warps per block where a row belongs to a warp
 
 // VEC elements as they lie in memory: 16 bytes, or one element where rows are not 16-byte aligned
@@ -1322,26 +1326,24 @@ ln_cols_kernel(const float* __restrict__ part, int P, int d, float* __restrict__
     }
 }
 
-// dw_c = sum_t dy_c xh_c and db_c = sum_t dy_c straight from the rows: 32 columns per block, a 32nd of
-// the rows per warp, four of them in flight, added in a fixed order
-template <typename T>
-__global__ void __launch_bounds__(1024)
-ln_few_cols_kernel(const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
-                   const T* __restrict__ dy, int Tn, int d, float* __restrict__ dw, float* __restrict__ db) {
+// dw_c = sum_t dy_c xh_c and db_c = sum_t dy_c straight from the rows: 32 columns per block, a W-th of the
+// rows per warp of its first W, four of them in flight, added in a fixed order
+template <int W, typename T>
+__device__ __forceinline__ void few_columns(const T* __restrict__ x, const float* __restrict__ mean,
+                                            const float* __restrict__ rstd, const T* __restrict__ dy, int Tn, int d,
+                                            float* __restrict__ dw, float* __restrict__ db, int block) {
     constexpr int U = 4;
-    __shared__ float sm[2][32][33];
-    // in this order: the row kernel that starts early behind this one reads what this one waited for
-    pdl_wait();
-    pdl_launch_next();
+    __shared__ float sm[2][W][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    if (warp >= W) return;
+    const int64_t c = (int64_t)block * 32 + lane;
     float sw = 0.f, sb = 0.f;
     if (c < d) {
-        for (int t = warp; t < Tn; t += 32 * U) {
+        for (int t = warp; t < Tn; t += W * U) {
             float xv[U], gv[U], mu[U], rs[U];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const int64_t row = t + 32 * j;
+                const int64_t row = t + W * j;
                 const bool in = row < Tn;
                 xv[j] = in ? to_f32(__ldg(x + row * d + c)) : 0.f;
                 gv[j] = in ? to_f32(__ldg(dy + row * d + c)) : 0.f;
@@ -1357,14 +1359,65 @@ ln_few_cols_kernel(const T* __restrict__ x, const float* __restrict__ mean, cons
     }
     sm[0][warp][lane] = sw;
     sm[1][warp][lane] = sb;
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" :: "n"(32 * W) : "memory");
     float* const out = warp == 0 ? dw : db;
     if (warp < 2 && c < d && out) {
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s += sm[warp][k][lane];
+        for (int k = 0; k < W; ++k) s += sm[warp][k][lane];
         out[c] = s;
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024)
+ln_few_cols_kernel(const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
+                   const T* __restrict__ dy, int Tn, int d, float* __restrict__ dw, float* __restrict__ db) {
+    // in this order: the row kernel that starts early behind this one reads what this one waited for
+    pdl_wait();
+    pdl_launch_next();
+    few_columns<32>(x, mean, rstd, dy, Tn, d, dw, db, blockIdx.x);
+}
+
+constexpr int FEW_WARPS = 16;            // of a column block below, and the least of a block
+
+// Both for few rows of up to 1024 vectors, in one launch: the first col_blocks blocks sum columns, the others
+// have a row each, one vector per thread of the first nthr.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(1024)
+ln_bwd_few_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
+                  const float* __restrict__ rstd, const T* __restrict__ dy, int Tn, int d, T* __restrict__ dx,
+                  float* __restrict__ dw, float* __restrict__ db, int col_blocks, int nthr) {
+    using P = Pack<T, VEC>;
+    __shared__ float buf[64 * 2];
+    pdl_launch_next();
+    pdl_wait();
+    if ((int)blockIdx.x < col_blocks) {
+        few_columns<FEW_WARPS>(x, mean, rstd, dy, Tn, d, dw, db, blockIdx.x);
+        return;
+    }
+    if ((int)threadIdx.x >= nthr) return;
+    const int64_t row = blockIdx.x - col_blocks;
+    const int c = threadIdx.x * VEC;
+    const bool in = c < d;
+    const typename P::raw xr = in ? P::load(x + row * d + c) : P::zero(), gr = in ? P::load(dy + row * d + c) : P::zero();
+    const float mu = __ldg(mean + row), rs = __ldg(rstd + row), inv_d = 1.0f / (float)d;
+    float xh[VEC], g[VEC], sums[2] = {0.f, 0.f};       // of g, of g xh; columns past d have dy = 0
+    P::unpack(xr, xh);
+    P::unpack(gr, g);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        xh[e] = (xh[e] - mu) * rs;
+        g[e] *= w && in ? __ldg(w + c + e) : 1.f;
+        sums[0] += g[e];
+        sums[1] = fmaf(g[e], xh[e], sums[1]);
+    }
+    int phase = 0;
+    group_sum<2, 0>(sums, buf, phase, nthr);
+    const float a = sums[0] * inv_d, k = sums[1] * inv_d;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) g[e] = rs * ((g[e] - a) - xh[e] * k);
+    if (in) P::store(dx + row * d + c, g);
 }
 
 bool rows16(const void* p) { return (uintptr_t)p % 16 == 0; }
@@ -1601,6 +1654,20 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
                       static_cast<const T*>(a.x), a.w, a.b, a.T, a.d, a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
 }
 
+// *done: the backward as one launch (ONE_LAUNCH_ROWS), for rows of up to 1024 vectors, or unaligned elements
+template <typename T>
+cudaError_t bwd_few(const LnArgs& a, bool aligned, bool* done) {
+    constexpr int V = Vec16<T>::VEC;
+    const bool vec = aligned && a.d % V == 0;
+    if (a.d > (vec ? 1024 * V : 1024)) return cudaSuccess;
+    *done = true;
+    const int nthr = ((vec ? a.d / V : a.d) + 31) / 32 * 32, threads = nthr > 32 * FEW_WARPS ? nthr : 32 * FEW_WARPS;
+    const int cols = a.part ? (a.d + 31) / 32 : 0, rows = a.dx ? (int)a.T : 0;
+    return launch_pdl(vec ? ln_bwd_few_kernel<T, V> : ln_bwd_few_kernel<T, 1>, dim3((unsigned)(cols + rows)),
+                      dim3((unsigned)threads), 0, a.stream, static_cast<const T*>(a.x), a.w, a.mean, a.rstd,
+                      static_cast<const T*>(a.dy), (int)a.T, a.d, static_cast<T*>(a.dx), a.dw, a.db, cols, nthr);
+}
+
 // As forward, but a block has two vectors per thread and two rows at a time up to 512 vectors, and three
 // (fp32, above 1024: six) and one above (T = 8192, bf16, d = 8192: 83 us, 142 with two; fp32 97, 172 with
 // four; odd widths, d = 6001: 101, 132 with two).  320 to 480 vectors: three and one, because two need six
@@ -1611,7 +1678,6 @@ cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
     constexpr int V = Vec16<T>::VEC;
     if (a.d % V == 0 && rows16(a.x) && rows16(a.dy) && rows16(a.dx)) {
         const int c = a.d / V;
-        if (c <= 1024 && a.T <= sms) return bwd<T, V, 1, 1, false>(a, blocks);
         constexpr int W = 32 * WARPS;
         if (c <= 8) return bwd_ring<T, 1, 2, 8, W>(a, blocks);
         if (c <= 16) return bwd_ring<T, 1, 2, 16, W>(a, blocks);
@@ -1663,6 +1729,12 @@ cudaError_t launch_layer_norm_backward(const LnArgs& args) {
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
     LnArgs a = args;
+    if (a.T <= ONE_LAUNCH_ROWS) {
+        const bool vec = rows16(a.x) && rows16(a.dy) && rows16(a.dx);
+        bool done = false;
+        e = a.dt == BF16 ? bwd_few<__nv_bfloat16>(a, vec, &done) : bwd_few<float>(a, vec, &done);
+        if (e != cudaSuccess || done) return e;
+    }
     a.late = a.part && a.T <= FEW_ROWS;
     if (a.late) {
         const dim3 grid((unsigned)(((int64_t)a.d + 31) / 32));
