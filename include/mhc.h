@@ -366,8 +366,9 @@ size_t mhc_linear_workspace_bytes(int64_t T, int K, int N, mhc_dtype dt);
  * Inputs : x [T,K], W [N,K] (dt); bias [N] fp32 or NULL; residual [T,N] (dt) or NULL.
  * Outputs: y [T,N] (dt); z [T,N] (dt), the pre-activation that mhc_linear_backward needs when
  *          act is not MHC_ACT_NONE, or NULL.
- * Products accumulate in fp32; bias, activation and residual are applied in fp32 before the
- * one rounding to dt.  Equal tokens of one call get equal bits, wherever they stand.
+ * Products accumulate in fp32 (fp32 ones with fp32's accuracy for operands of any magnitude, and
+ * fastest while operands stay below 2^112 and sums below 2^94); bias, activation and residual are
+ * applied in fp32 before the one rounding to dt.  Equal tokens of one call get equal bits, wherever they stand.
  * workspace: 256-byte aligned, at least mhc_linear_workspace_bytes(T, K, N, dt) bytes
  *          (MHC_ERR_WORKSPACE); may be NULL when that is 0.
  * Errors : MHC_ERR_UNSUPPORTED for an act that is not an mhc_act value.

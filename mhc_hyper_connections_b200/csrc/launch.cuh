@@ -234,11 +234,13 @@ cudaError_t launch_gemm_thin(const GemmArgs& a);
 bool gemm_tc_ok(const GemmArgs& a);
 cudaError_t launch_gemm_tc(const GemmArgs& a);
 // An fp32 product on the tensor cores from its operands' bf16 parts (split_rows in linear.cu): three
-// planes of rows of lda (ldb) elements, a_plane (b_plane) elements apart, for the same layouts.
+// planes of rows of lda (ldb) elements, a_plane (b_plane) elements apart, for the same layouts, of the values
+// times 2^16.  *over, 0 at the launch, is set where a sum is too large to be formed so.
 struct F32Planes {
     const void* A;
     const void* B;
     int64_t lda, ldb, a_plane, b_plane;
+    int* over;
 };
 cudaError_t launch_gemm_f32(const GemmArgs& a, const F32Planes& f);
 // Scratch of the two, 256-byte aligned, and the modelled time of the second in us.

@@ -192,13 +192,16 @@ cudaError_t product(const GemmArgs& g) {
     return gemm_thin_ok(g) ? launch_gemm_thin(g) : launch_gemm_generic(g);
 }
 
-// The bf16 parts h + m + l of fp32 rows, in three planes of rows on 16-byte boundaries.  A value that
-// is not finite, or whose h would not be, has no such parts: its block sets its word of `odd`, and the
-// CUDA-core kernel forms the product instead.
+// The bf16 parts h + m + l of fp32 rows times 2^16, in three planes of rows on 16-byte boundaries.  The
+// scale makes the parts exact for small values too: fp32's last place is never below 2^-149, bf16's smallest
+// number is 2^-133 (without it values below 2^-110 lost bits: a relative error of 2.7e-5 at 1e-36).  A value
+// that is not finite, or whose h would not be (from 2^112 on), has no such parts: its block sets its word of
+// `odd`, and the CUDA-core kernel forms the product instead.
 struct SplitJob {
     const float* src;
     __nv_bfloat16* dst;
     int* odd;                          // SPLIT_BLOCKS words
+    int* clear;                        // a word to set to 0: F32Planes::over of a product of these rows
     int64_t rows, ld;                  // ld: elements per row of a plane, a multiple of 8
     int cols;
 };
@@ -226,6 +229,7 @@ __global__ void __launch_bounds__(256) split_rows_kernel(const __grid_constant__
         float h[8], m[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
+            f[e] *= 65536.0f;
             h[e] = __bfloat162float(__float2bfloat16_rn(f[e]));
             odd |= !(fabsf(h[e]) <= 3.4028234e38f);
             f[e] -= h[e];                              // exact, as is the next difference
@@ -238,7 +242,10 @@ __global__ void __launch_bounds__(256) split_rows_kernel(const __grid_constant__
         st_v4(d + 2 * plane, Vec16<__nv_bfloat16>::pack(f));
     }
     odd = __syncthreads_or(odd);
-    if (threadIdx.x == 0) j.odd[blockIdx.x] = odd;
+    if (threadIdx.x == 0) {
+        j.odd[blockIdx.x] = odd;
+        if (blockIdx.x == 0) *j.clear = 0;
+    }
 }
 
 // every block writes its word, so all SPLIT_BLOCKS of them are set afterwards
@@ -280,7 +287,7 @@ Regions regions(int64_t T, int K, int N, DType dt, bool backward) {
         L.x = take((size_t)T * L.ldk * (L.parts ? 6 : 2));
         L.W = take((size_t)N * L.ldk * (L.parts ? 6 : 2));
     }
-    if (L.parts) L.odd = take((size_t)3 * SPLIT_BLOCKS * 4);
+    if (L.parts) L.odd = take((size_t)(3 * SPLIT_BLOCKS + 2) * 4);
     if (backward) {
         L.dz = take((size_t)T * (dt == BF16 ? L.ldn : N) * es);
         L.part = take((size_t)dz_runs(T, N) * N * 4);
@@ -314,13 +321,14 @@ cudaError_t launch_linear(const LinearArgs& a) {
     __nv_bfloat16* xc = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
     __nv_bfloat16* wc = reinterpret_cast<__nv_bfloat16*>(ws + L.W);
     if (L.parts) {
-        int* odd = reinterpret_cast<int*>(ws + L.odd);
-        const SplitJob x{static_cast<const float*>(a.x), xc, odd, a.T, L.ldk, a.K};
-        const SplitJob w{static_cast<const float*>(a.W), wc, odd + SPLIT_BLOCKS, a.N, L.ldk, a.K};
+        int* over = reinterpret_cast<int*>(ws + L.odd);      // and the words of x and W after it
+        int* odd = over + 1;
+        const SplitJob x{static_cast<const float*>(a.x), xc, odd, over, a.T, L.ldk, a.K};
+        const SplitJob w{static_cast<const float*>(a.W), wc, odd + SPLIT_BLOCKS, over, a.N, L.ldk, a.K};
         cudaError_t e = split_rows(x, w, a.stream);
         if (e == cudaSuccess)
-            e = launch_gemm_f32(g, F32Planes{xc, wc, L.ldk, L.ldk, a.T * L.ldk, a.N * L.ldk});
-        return e == cudaSuccess ? launch_gemm_generic(g, odd, 2 * SPLIT_BLOCKS) : e;
+            e = launch_gemm_f32(g, F32Planes{xc, wc, L.ldk, L.ldk, a.T * L.ldk, a.N * L.ldk, over});
+        return e == cudaSuccess ? launch_gemm_generic(g, over, 1 + 2 * SPLIT_BLOCKS) : e;
     }
     if (L.pad) {
         const PadJob x{static_cast<const __nv_bfloat16*>(a.x), xc, a.T, L.ldk, a.K};
@@ -350,11 +358,14 @@ cudaError_t launch_linear_backward(const LinearArgs& a) {
     __nv_bfloat16* xc = reinterpret_cast<__nv_bfloat16*>(ws + L.x);
     __nv_bfloat16* wc = reinterpret_cast<__nv_bfloat16*>(ws + L.W);
     __nv_bfloat16* zc = reinterpret_cast<__nv_bfloat16*>(ws + L.dzp);
-    int* odd = reinterpret_cast<int*>(ws + L.odd);       // of W, dz, x
+    // the words of dx's product: its over, W's, dz's; and of dW's: dz's, x's, its over
+    int* const words = reinterpret_cast<int*>(ws + L.odd);
+    int *const odd = words + 1, *const over_dW = odd + 3 * SPLIT_BLOCKS;
     if (L.parts) {
-        const SplitJob jw{static_cast<const float*>(a.W), wc, odd, a.N, L.ldk, a.K};
-        const SplitJob jz{static_cast<const float*>(dz ? dz : a.dy), zc, odd + SPLIT_BLOCKS, a.T, L.ldn, a.N};
-        const SplitJob jx{static_cast<const float*>(a.x), xc, odd + 2 * SPLIT_BLOCKS, a.T, L.ldk, a.K};
+        int* const over_z = a.dx ? words : over_dW;      // also cleared with the other operand's rows
+        const SplitJob jw{static_cast<const float*>(a.W), wc, odd, words, a.N, L.ldk, a.K};
+        const SplitJob jz{static_cast<const float*>(dz ? dz : a.dy), zc, odd + SPLIT_BLOCKS, over_z, a.T, L.ldn, a.N};
+        const SplitJob jx{static_cast<const float*>(a.x), xc, odd + 2 * SPLIT_BLOCKS, over_dW, a.T, L.ldk, a.K};
         e = split_rows(jz, a.dx ? jw : jx, a.stream);
         if (e == cudaSuccess && a.dx && a.dW) e = split_rows(jx, SplitJob{}, a.stream);
     } else if (L.pad) {
@@ -371,23 +382,23 @@ cudaError_t launch_linear_backward(const LinearArgs& a) {
     g.b_mn = true;
     g.ldb = L.pad ? L.ldk : a.K;
     // one of the two products, with the words of its operands
-    auto run = [&](const void* B, const __nv_bfloat16* parts, int64_t b_rows, const int* words) {
+    auto run = [&](const void* B, const __nv_bfloat16* parts, int64_t b_rows, const int* first, int* over) {
         g.B = L.pad ? parts : B;
         if (!L.parts) return product(g);
-        cudaError_t r = launch_gemm_f32(g, F32Planes{zc, parts, L.ldn, L.ldk, a.T * L.ldn, b_rows * L.ldk});
-        if (r == cudaSuccess) r = launch_gemm_generic(g, words, 2 * SPLIT_BLOCKS);
+        cudaError_t r = launch_gemm_f32(g, F32Planes{zc, parts, L.ldn, L.ldk, a.T * L.ldn, b_rows * L.ldk, over});
+        if (r == cudaSuccess) r = launch_gemm_generic(g, first, 1 + 2 * SPLIT_BLOCKS);
         return r;
     };
     if (a.dx) {                              // dx[t][k] = sum_n dz[t][n] W[n][k]
         g.M = a.T; g.N = a.K; g.K = a.N;
         g.D = a.dx;
-        e = run(a.W, wc, a.N, odd);
+        e = run(a.W, wc, a.N, words, words);
     }
     if (e == cudaSuccess && a.dW) {          // dW[n][k] = sum_t dz[t][n] x[t][k]
         g.a_mn = true;
         g.M = a.N; g.N = a.K; g.K = a.T;
         g.D = a.dW;
-        e = run(a.x, xc, a.T, odd + SPLIT_BLOCKS);
+        e = run(a.x, xc, a.T, odd + SPLIT_BLOCKS, over_dW);
     }
     return e;
 }

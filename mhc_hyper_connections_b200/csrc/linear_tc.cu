@@ -619,6 +619,10 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
 // short (CHUNK blocks of 64), and the five small products have an accumulator of their own, where the
 // dropped bits are 2^-8 of those of h h (one accumulator for all six: a relative error of 1.5e-6 at
 // any K; see linear.cu for when this kernel runs).
+//
+// The parts are those of the values times 2^16 (SplitJob), so the sums are 2^32 times what they stand for.
+// One of 2^126 or more (2^94, 2e28, of the product's) has overflowed on the way or may have: it sets *over,
+// and the CUDA-core kernel behind this one forms the product.
 
 struct F32Cfg {
     static constexpr int BN = 128;
@@ -629,6 +633,7 @@ struct F32Cfg {
     static constexpr int SMEM = NS * STAGE + OUT + 1024;
     static constexpr int TMEM_COLS = 512;
     static constexpr int CHUNK = 4;
+    static constexpr float UNSCALE = 0x1p-32f, OVER = 0x1p126f;
     static_assert(SMEM <= 232448 - 512, "shared memory");
     static_assert(BN == 4 * CW, "a block per epilogue warp");
 };
@@ -638,7 +643,7 @@ struct F32Cfg {
 template <bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue<float> ep, int64_t M, int64_t N,
-                const __grid_constant__ Work work, Limits lim) {
+                const __grid_constant__ Work work, Limits lim, int* __restrict__ over) {
     using C = F32Cfg;
     constexpr int NS = C::NS, BN = C::BN;
     extern __shared__ unsigned char smem_raw[];
@@ -786,6 +791,13 @@ gemm_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilo
             }
             if (!ok) break;
             if (c0 >= N || r0 >= M) continue;
+            bool large = false;
+#pragma unroll
+            for (int j = 0; j < CW; ++j) {
+                large |= !(fabsf(sum[j]) < C::OVER);
+                sum[j] *= C::UNSCALE;
+            }
+            if (large) *over = 1;
             if (it.block < 0)
                 finish_block<float>(ep, maps, sum, out, r0, c0, M, N, lane);
             else
@@ -1145,8 +1157,8 @@ Work work_of(int64_t M, int64_t N, int64_t K, int bn, int S) {
 }
 
 // The pair kernel on its work, and the sums of the shared tiles after it
-template <typename T, int BN, typename K>
-cudaError_t launch_pairs(K kern, int smem, Maps& maps, const GemmArgs& g, int S, int sms) {
+template <typename T, int BN, typename K, typename... More>
+cudaError_t launch_pairs(K kern, int smem, Maps& maps, const GemmArgs& g, int S, int sms, More... more) {
     cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
     const Epilogue<T> ep = epilogue_of<T>(g);
@@ -1155,7 +1167,8 @@ cudaError_t launch_pairs(K kern, int smem, Maps& maps, const GemmArgs& g, int S,
     if (!output_maps(&maps, ep, g.M, g.N) || (shared && !make_map_parts(&maps.p, g.part, shared, BN)))
         return cudaErrorInvalidValue;
     const unsigned grid = 2u * (unsigned)(w.items < pairs ? w.items : pairs);
-    e = launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)smem, g.stream, maps, ep, g.M, g.N, w, limits());
+    e = launch_pdl(kern, dim3(grid), dim3(PAIR_THREADS), (size_t)smem, g.stream, maps, ep, g.M, g.N, w, limits(),
+                   more...);
     if (e != cudaSuccess || !shared) return e;
     return launch_pdl(join_kernel<T, BN>, dim3(BN / 4, (unsigned)(shared / S)), dim3(256), 0, g.stream,
                       static_cast<const float*>(g.part), ep, g.M, g.N, w);
@@ -1182,7 +1195,7 @@ cudaError_t f32_launch(const GemmArgs& g, const F32Planes& f, int S, int sms) {
     if (!make_map_planes(&maps.a, f.A, g.M, g.K, f.lda, f.a_plane, A_MN, 128) ||
         !make_map_planes(&maps.b, f.B, g.N, g.K, f.ldb, f.b_plane, B_MN, BN / 2))
         return cudaErrorInvalidValue;
-    return launch_pairs<float, BN>(gemm_f32_kernel<A_MN, B_MN>, F32Cfg::SMEM, maps, g, S, sms);
+    return launch_pairs<float, BN>(gemm_f32_kernel<A_MN, B_MN>, F32Cfg::SMEM, maps, g, S, sms, f.over);
 }
 
 template <int BN, bool A_MN, bool B_MN>
