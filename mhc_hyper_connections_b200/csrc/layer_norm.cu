@@ -9,7 +9,8 @@
 // Both are bound by HBM: 2 T d elements forward, 3 T d backward, a few operations each.  So each
 // row is read once and kept in registers, packed as it was stored, between its reduction and its
 // output; sums are fp32, and the variance is summed around the mean (a second walk over the
-// registers), which a mean far from zero does not spoil.
+// registers), which a mean far from zero does not spoil.  Where the mean's own roundings would show, a third
+// walk takes them off (off_centre).
 //
 // A row belongs to 8, 16 or 32 lanes or to a thread block.  A thread owns the same NV vectors of VEC
 // columns in every row it sees, so w and b are loaded once and the backward's column sums stay in
@@ -96,6 +97,47 @@ __device__ __forceinline__ void group_sum(float (&v)[R], float* buf, int& phase,
     }
 }
 
+// The first mean carries the roundings of its sum.  In a row of nearly equal values far from zero they make up
+// most of x - mean and of the variance (12345.678 throughout with eps = 1e-5 gave y = 0.3, and bf16 100
+// throughout, d = 1000, eps = 1e-12, gave y = 1).  Such rows, |mean| above 64 standard deviations, are walked
+// once more for the sum t of x - mean: the mean moves by t / d, and the sum of squares s falls by t^2 / d.  The
+// division (not a product with 1 / d) makes both exact for a row of one value: y = b, rstd = 1 / sqrt(eps).
+// Summing t for every row in the second walk took up to a tenth more time (T = 8192, d = 5000, bf16: 46.7 us,
+// 41.8 without).
+__device__ __forceinline__ bool off_centre(float mean, float s, float inv_d) {
+    return mean * mean * 0x1p-12f > s * inv_d;           // false for rows that are not finite
+}
+__device__ __forceinline__ void centre(float& mean, float& s, float t, int d) {
+    const float m1 = t / (float)d;
+    mean += m1;
+    s = fmaxf(fmaf(-t, m1, s), 0.f);
+}
+// Such a row in the kernels that hold many registers per thread: the walk over memory, not inlined, so that the
+// loop around it keeps its registers (T = 8192, d = 8192, fp32: 83 us, 96 with a walk over registers).  nthr
+// threads share the row, VEC elements at a time, G as in group_sum (buf: 32 floats for G = 0).
+template <typename T, int VEC, int G>
+__device__ __noinline__ float2 recentre(const T* __restrict__ row, int d, int idx, int nthr, float mean, float s,
+                                        float* buf) {
+    float t = 0.f;
+    for (int c = idx * VEC; c < d; c += nthr * VEC) {
+        float f[VEC];
+        Pack<T, VEC>::unpack(Pack<T, VEC>::load(row + c), f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) t += f[e] - mean;
+    }
+#pragma unroll
+    for (int o = (G ? G : 32) / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if constexpr (G == 0) {
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = t;
+        asm volatile("bar.sync 1, %0;" :: "r"(nthr) : "memory");
+        t = 0.f;
+        for (int w = 0; w < nthr >> 5; ++w) t += buf[w];
+        asm volatile("bar.sync 1, %0;" :: "r"(nthr) : "memory");      // before it is written again
+    }
+    centre(mean, s, t, d);
+    return make_float2(mean, s);
+}
+
 // threads of a block: a warp per row uses WARPS warps; a block per row as many threads as the row
 // needs, up to 1024 with one vector each (few rows) and 512 with more, which the registers allow
 // The wait for the kernels before this one: ahead of its reads, or (late) at its end, for a kernel
@@ -120,7 +162,7 @@ ln_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
                               int64_t Tn, int d, float eps, T* __restrict__ y, float* __restrict__ mean_out,
                               float* __restrict__ rstd_out) {
     using P = Pack<T, VEC>;
-    __shared__ float buf[WARP ? 1 : 64 * R];
+    __shared__ float buf[WARP ? 1 : 64 * R], far[WARP ? 1 : 32];
     int phase = 0;
     pdl_launch_next();
     pdl_wait();
@@ -184,6 +226,25 @@ ln_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
         group_sum<R, WARP ? 32 : 0>(s, buf, phase, nthr);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            if (!off_centre(mean[r], s[r], inv_d)) continue;      // the same in the whole group; rows past Tn are 0
+            if constexpr (NV == 1) {
+                float t[1] = {0.f}, f[VEC];
+                P::unpack(raw[r][0], f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (idx * VEC < d) t[0] += f[e] - mean[r];
+                static_assert(R == 1, "buf has room for R values");
+                group_sum<1, WARP ? 32 : 0>(t, buf, phase, nthr);
+                centre(mean[r], s[r], t[0], d);
+            } else {
+                const float2 m = recentre<T, VEC, WARP ? 32 : 0>(x + (row0 + r * groups) * d, d, idx, nthr, mean[r],
+                                                                 s[r], far);
+                mean[r] = m.x;
+                s[r] = m.y;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
             const int64_t row = row0 + r * groups;
             if (row >= Tn) break;
             const float rstd = 1.0f / sqrtf(fmaf(s[r], inv_d, eps));
@@ -210,7 +271,7 @@ __global__ void __launch_bounds__(1024)
 ln_fwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
                                    const float* __restrict__ b, int64_t Tn, int d, float eps, T* __restrict__ y,
                                    float* __restrict__ mean_out, float* __restrict__ rstd_out) {
-    __shared__ float buf[64];
+    __shared__ float buf[64], far[32];
     int phase = 0;
     pdl_launch_next();
     pdl_wait();
@@ -220,13 +281,18 @@ ln_fwd_long_kernel(const T* __restrict__ x, const float* __restrict__ w,
         float s[1] = {0.f};
         for (int c = threadIdx.x; c < d; c += blockDim.x) s[0] += to_f32(__ldg(xr + c));
         group_sum<1, 0>(s, buf, phase, blockDim.x);
-        const float mean = s[0] * inv_d;
+        float mean = s[0] * inv_d;
         s[0] = 0.f;
         for (int c = threadIdx.x; c < d; c += blockDim.x) {
             const float v = to_f32(__ldg(xr + c)) - mean;
             s[0] = fmaf(v, v, s[0]);
         }
         group_sum<1, 0>(s, buf, phase, blockDim.x);
+        if (off_centre(mean, s[0], inv_d)) {
+            const float2 m = recentre<T, 1, 0>(xr, d, threadIdx.x, blockDim.x, mean, s[0], far);
+            mean = m.x;
+            s[0] = m.y;
+        }
         const float rstd = 1.0f / sqrtf(fmaf(s[0], inv_d, eps));
         for (int c = threadIdx.x; c < d; c += blockDim.x)
             store_elem(y + row * d + c, fmaf((to_f32(__ldg(xr + c)) - mean) * rstd, w ? __ldg(w + c) : 1.f,
@@ -536,7 +602,7 @@ ln_fwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(8) uint64_t bars[2 * MAX_SLOTS];
     __shared__ int abort_flag;
-    __shared__ __align__(16) float buf[G ? 1 : 64 * R];
+    __shared__ __align__(16) float buf[G ? 1 : 64 * R], far[G ? 1 : 32];
     int phase = 0;
     const int consumers = blockDim.x - 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) ring_init(bars, &abort_flag, slots, consumers >> 5);
@@ -597,6 +663,41 @@ ln_fwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
             s[r] = acc.x + acc.y;
         }
         group_sum<R, G>(s, buf, phase, nthr);
+        if constexpr (G != 0) {
+            bool off = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) off |= off_centre(mean[r], s[r], inv_d);
+            if (__any_sync(0xffffffffu, off)) {
+                float t[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float2 acc = both(0.f);
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        if ((v * nthr + idx) * VEC >= d) continue;
+                        float2 f[HV];
+                        pairs_of(raw[r][v], f);
+#pragma unroll
+                        for (int e = 0; e < HV; ++e) acc = __fadd2_rn(acc, __fadd2_rn(f[e], both(-mean[r])));
+                    }
+                    t[r] = acc.x + acc.y;
+                }
+                group_sum<R, G>(t, buf, phase, nthr);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (off_centre(mean[r], s[r], inv_d)) centre(mean[r], s[r], t[r], d);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t row = i * B + r;
+                if (row < Tn && off_centre(mean[r], s[r], inv_d)) {
+                    const float2 m = recentre<T, VEC, 0>(x + row * d, d, idx, nthr, mean[r], s[r], far);
+                    mean[r] = m.x;
+                    s[r] = m.y;
+                }
+            }
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = i * B + first + r;
@@ -632,11 +733,13 @@ ln_fwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
 // a ring of its own that it refills as soon as a row is in registers.  The 32-byte pieces of w and b
 // that go with a bf16 vector are stored as two planes of 16 bytes per lane, which reads without bank
 // conflicts.
-// blocks of 256 threads per SM, as many as the registers of a row per warp allow
-template <int NV> constexpr int WARP_BLOCKS = NV > 10 ? 1 : NV > 8 ? 2 : NV > 4 ? 3 : 4;
+// blocks of 256 threads per SM, as many as the registers of a row per warp allow (bf16, 8 vectors, T = 16384:
+// d = 2048 22.3 us with two and 25.2 with three, d = 1537 29.5 and 33.8; fp32, d = 1024 20.9 and 19.7)
+template <typename T, int NV>
+constexpr int WARP_BLOCKS = NV > 10 ? 1 : NV > 8 || (NV == 8 && sizeof(T) == 2) ? 2 : NV > 4 ? 3 : 4;
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(256, WARP_BLOCKS<NV>)
+__global__ void __launch_bounds__(256, WARP_BLOCKS<T, NV>)
 ln_fwd_warp_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int64_t Tn, int d,
                    float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots,
                    Limits lim) {
@@ -711,7 +814,7 @@ ln_fwd_warp_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
         float s = (a0.x + a0.y) + (a1.x + a1.y);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float mean = s * inv_d;
+        float mean = s * inv_d;
         a0 = a1 = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -728,6 +831,21 @@ ln_fwd_warp_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
         s = (a0.x + a0.y) + (a1.x + a1.y);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (off_centre(mean, s, inv_d)) {
+            a0 = both(0.f);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if ((v * 32 + lane) * VEC >= d) continue;
+                float2 f[HV];
+                pairs_of(raw[v], f);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) a0 = __fadd2_rn(a0, __fadd2_rn(f[e], both(-mean)));
+            }
+            float t = a0.x + a0.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            centre(mean, s, t, d);
+        }
         const float rstd = 1.0f / sqrtf(fmaf(s, inv_d, eps));
         T* yr = y + row * d + lane * VEC;
 #pragma unroll
@@ -983,7 +1101,7 @@ __device__ __forceinline__ uint4 masked(uint4 v, uint4 m) {
 
 // ln_fwd_warp_kernel for such rows; gridDim.x is a multiple of 8
 template <typename T, int NV>
-__global__ void __launch_bounds__(256, WARP_BLOCKS<NV>)
+__global__ void __launch_bounds__(256, WARP_BLOCKS<T, NV>)
 ln_fwd_shift_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int64_t Tn, int d,
                     float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots,
                     Limits lim) {
@@ -1070,7 +1188,7 @@ ln_fwd_shift_kernel(const T* __restrict__ x, const float* __restrict__ w, const 
         float sum = (a0.x + a0.y) + (a1.x + a1.y);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float mean = sum * inv_d;
+        float mean = sum * inv_d;
         a0 = a1 = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -1091,6 +1209,26 @@ ln_fwd_shift_kernel(const T* __restrict__ x, const float* __restrict__ w, const 
         sum = (a0.x + a0.y) + (a1.x + a1.y);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (off_centre(mean, sum, inv_d)) {
+            a0 = both(0.f);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (v * 32 + lane >= nw) continue;
+                float2 f[HV];
+                pairs_of(raw[v], f);
+#pragma unroll
+                for (int e = 0; e < HV; ++e) {
+                    f[e] = __fadd2_rn(f[e], both(-mean));
+                    if (v == 0) f[e] = __fmul2_rn(f[e], keep0[e]);
+                    if (v == vl) f[e] = __fmul2_rn(f[e], keep1[e]);
+                    a0 = __fadd2_rn(a0, f[e]);
+                }
+            }
+            float t = a0.x + a0.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            centre(mean, sum, t, d);
+        }
         const float rstd = 1.0f / sqrtf(fmaf(sum, inv_d, eps));
         unsigned char* yr = reinterpret_cast<unsigned char*>(y) + sx.at(row);
         uint4 end0 = make_uint4(0, 0, 0, 0), end1 = end0;      // words that are not wholly the row's
@@ -1541,7 +1679,7 @@ cudaError_t fwd_warp(const LnArgs& a) {
     auto kern = ln_fwd_warp_kernel<T, NV>;
     // the SM's shared memory in equal parts
     const size_t wb = (size_t)2 * NV * 32 * Vec16<T>::VEC * 4, slot = (size_t)(TH / 32) * a.d * sizeof(T);
-    int slots = (int)((ROOM / WARP_BLOCKS<NV> - wb) / slot);
+    int slots = (int)((ROOM / WARP_BLOCKS<T, NV> - wb) / slot);
     slots = slots < 1 ? 1 : slots > WARP_SLOTS ? WARP_SLOTS : slots;
     const size_t smem = wb + slots * slot;
     cudaError_t e = allow_room(kern);
@@ -1561,7 +1699,7 @@ cudaError_t fwd_shift(const LnArgs& a) {
     auto kern = ln_fwd_shift_kernel<T, NV>;
     const size_t wb = (size_t)2 * NV * 32 * Vec16<T>::VEC * 4;
     const size_t slot = (size_t)(TH / 32) * ((a.d * sizeof(T) + 15) / 16 * 16 + 16);
-    int slots = (int)((ROOM / WARP_BLOCKS<NV> - wb) / slot);
+    int slots = (int)((ROOM / WARP_BLOCKS<T, NV> - wb) / slot);
     slots = slots < 1 ? 1 : slots > WARP_SLOTS ? WARP_SLOTS : slots;
     const size_t smem = wb + slots * slot;
     cudaError_t e = allow_room(kern);
