@@ -453,6 +453,7 @@ def mhc_backward_noalloc(X, F_out, phi, b_pre, b_post, b_res, alpha_pre, alpha_p
 
 
 _torch = None
+_INT_MAX = (1 << 31) - 1
 
 
 def _bind_torch():
@@ -470,7 +471,28 @@ def _rows(where, name, t):
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{where}: {name} must be two-dimensional, has shape {tuple(shape)}")
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:
+        _within(where, name, shape)
     return shape
+
+
+def _within(where, name, shape):
+    """Widths and feature counts are C ints, token counts 64 bits: ctypes would drop the bits above."""
+    if shape[1] > _INT_MAX or (name == "W" and shape[0] > _INT_MAX):
+        raise MhcError(2, where, f"{name} has shape {tuple(shape)}, past the library's largest")
+
+
+def _size(fn, T, *rest):
+    """A workspace query; 0, as for every shape the library rejects, where a value does not fit its C type."""
+    if not -_INT_MAX <= min(rest) <= max(rest) <= _INT_MAX or abs(T) >> 62:
+        return 0
+    return int(fn(T, *rest))
+
+
+def _act(act) -> int:
+    """An activation as the C ABI takes it; what is none of them as one it refuses."""
+    act = int(act)
+    return act if ACT_NONE <= act <= ACT_SILU else -1
 
 
 def _pointers(where, dev, specs):
@@ -540,7 +562,7 @@ def mhc_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
 
 def mhc_layer_norm_backward_workspace_bytes(T: int, d: int) -> int:
     """Bytes of device workspace mhc_layer_norm_backward needs (0 for T = 0 and rejected shapes)."""
-    return int(load_library().mhc_layer_norm_backward_workspace_bytes(int(T), int(d)))
+    return _size(load_library().mhc_layer_norm_backward_workspace_bytes, int(T), int(d))
 
 
 def mhc_layer_norm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, workspace=None, stream=None):
@@ -573,7 +595,7 @@ def _dt_of(dtype) -> int:
 
 def mhc_linear_workspace_bytes(T: int, K: int, N: int, dtype) -> int:
     """Bytes of device workspace mhc_linear needs for x [T, K] and W [N, K] (0: none)."""
-    return int(load_library().mhc_linear_workspace_bytes(int(T), int(K), int(N), _dt_of(dtype)))
+    return _size(load_library().mhc_linear_workspace_bytes, int(T), int(K), int(N), _dt_of(dtype))
 
 
 def mhc_linear(x, W, bias, y, act: int = ACT_NONE, residual=None, z=None, workspace=None, stream=None):
@@ -593,12 +615,12 @@ def mhc_linear(x, W, bias, y, act: int = ACT_NONE, residual=None, z=None, worksp
         ("residual", residual, out, xt), ("y", y, out, xt), ("z", z, out, xt)))
     ws, nbytes = _workspace(workspace, dev)
     _call(where, load_library().mhc_linear, dev, stream,
-          (px, pw, pb, pr, T, K, N, int(act), dt, py, pz, ws, nbytes))
+          (px, pw, pb, pr, T, K, N, _act(act), dt, py, pz, ws, nbytes))
 
 
 def mhc_linear_backward_workspace_bytes(T: int, K: int, N: int, dtype) -> int:
     """Bytes of device workspace mhc_linear_backward needs for x [T, K] and W [N, K]."""
-    return int(load_library().mhc_linear_backward_workspace_bytes(int(T), int(K), int(N), _dt_of(dtype)))
+    return _size(load_library().mhc_linear_backward_workspace_bytes, int(T), int(K), int(N), _dt_of(dtype))
 
 
 def mhc_linear_backward(x, W, z, dy, dx, dW, dbias, workspace, act: int = ACT_NONE, stream=None):
@@ -616,7 +638,7 @@ def mhc_linear_backward(x, W, z, dy, dx, dW, dbias, workspace, act: int = ACT_NO
         ("dW", dW, (N, K), xt), ("dbias", dbias, (N,), f32)))
     ws, nbytes = _workspace(workspace, dev)
     _call(where, load_library().mhc_linear_backward, dev, stream,
-          (px, pw, pz, T, K, N, int(act), dt, pg, pdx, pdw, pdb, ws, nbytes))
+          (px, pw, pz, T, K, N, _act(act), dt, pg, pdx, pdw, pdb, ws, nbytes))
 
 
 def mhc_amax_gain(H_layers, gain, stream=None):
