@@ -461,7 +461,9 @@ mhc_status mhc_debug_backward_stop_after(int32_t stages, uint32_t wait_limit_us)
 /*
  * mhc_debug_sublayer_stop_after -- test hook for the failure path of the sub-layer operators: the
  * tensor-core products of mhc_linear and mhc_linear_backward, and the layer norm kernels that
- * bring rows into shared memory (16-byte-aligned rows, more of them than SMs).  After this call
+ * bring rows into shared memory (rows of a multiple of 16 bytes, up to 32 KB forward and 16 KB (bf16)
+ * or 32 KB (fp32) backward, more of them than SMs forward and than 256 backward; other rows of 257
+ * elements to 16 KB, from 16 per SM on; the arrays 16-byte aligned).  After this call
  * their launches stop loading after `stages` stages per CTA, or batches of rows per ring
  * (stages < 0: never, the default), and give up a wait after `wait_limit_us` microseconds
  * (default 1000000; accepted range 1000 .. 10000000, else MHC_ERR_SHAPE).  The waits for what is
