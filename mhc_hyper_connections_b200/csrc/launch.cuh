@@ -226,6 +226,7 @@ struct GemmArgs {
 };
 // Where only_if is given, the kernel does nothing unless one of its only_if_n words is set.
 cudaError_t launch_gemm_generic(const GemmArgs& a, const int* only_if = nullptr, int only_if_n = 0);
+double gemm_generic_time(int64_t M, int64_t N, int64_t K);      // in us, of an fp32 product
 // The same for up to 8 rows of A (linear_thin.cu), for products gemm_thin_ok accepts.
 bool gemm_thin_ok(const GemmArgs& a);
 cudaError_t launch_gemm_thin(const GemmArgs& a);

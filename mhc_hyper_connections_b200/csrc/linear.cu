@@ -253,17 +253,21 @@ cudaError_t split_rows(const SplitJob& a, const SplitJob& b, cudaStream_t s) {
     return launch_pdl(split_rows_kernel, dim3(SPLIT_BLOCKS, b.rows ? 2 : 1), dim3(256), 0, s, a, b);
 }
 
-// fp32 products that go to the tensor cores: those whose time on CUDA cores exceeds that of the parts and
-// their products, by these times in us (measured, operands in L2): CUDA cores 7 us and 27 TFLOP/s; the parts
-// 10 bytes per element at 5.5 TB/s and 8.5 us for their launch and the one that forms values without parts,
-// 9 more in a backward call, which decides for its two products together.  T = 192, 4096 -> 1024: 75 us on CUDA
-// cores, 31 from parts; T = 512, 512 -> 512: 14 and 17.
+// fp32 products that go to the tensor cores: those whose time on CUDA cores exceeds that of the parts and their
+// products, by these models in us (measured, operands in L2).  The parts: 10 bytes per element at 7.5 TB/s, at
+// 2.9 past 64 MB, and 8.5 us for their launch and the one that forms values without parts, 9 more in a backward
+// call, which decides for its two products together.  Up to 16 tokens CUDA cores are faster throughout.  Parts
+// and CUDA cores, forward: T = 24, 4096 -> 1024 28 and 42, 1024 -> 4096 28 and 22; T = 64, 4096 -> 4096 94 and 77;
+// T = 65 94 and 149; T = 512, 512 -> 512 17 and 14; backward: T = 24, 1024 -> 4096 50 and 88, 4096 -> 1024 49 and
+// 41.  Of 260 calls (gemm_generic_time's shapes) three take the slower form by more than a tenth, all backward:
+// T = 64, 4096 -> 1024 58 for 50; 512 -> 2048, T = 48 40 for 35, T = 24 38 for 34.
 bool parts_pay(int64_t T, int K, int N, bool backward) {
     if (T <= 16 || T >= ((int64_t)1 << 31) - 1024) return false;
-    const double cores = 7.0 + 2.0 * (double)T * K * N / 27e6;
-    const double split = ((double)T * K + (double)N * K + (backward ? (double)T * N : 0.0)) * 10.0 / 5.5e6 + 8.5;
-    if (!backward) return split + gemm_f32_time(T, N, K, false) < cores;
-    return split + 9.0 + gemm_f32_time(T, K, N, false) + gemm_f32_time(N, K, T, true) < 2.0 * cores;
+    const double bytes = 10.0 * ((double)T * K + (double)N * K + (backward ? (double)T * N : 0.0));
+    const double split = bytes / 7.5e6 + std::max(0.0, bytes - 64e6) / 4.6e6 + 8.5;
+    if (!backward) return split + gemm_f32_time(T, N, K, false) < gemm_generic_time(T, N, K);
+    return split + 9.0 + gemm_f32_time(T, K, N, false) + gemm_f32_time(N, K, T, true) <
+           gemm_generic_time(T, K, N) + gemm_generic_time(N, K, T);
 }
 
 // Regions of the workspaces, in bytes.  bf16 rows of K elements that are not a multiple of 16 bytes

@@ -240,24 +240,32 @@ cudaError_t launch(const GemmArgs& g, int S, const int* only_if, int only_if_n) 
                               vec(g.D, g.N) && vec(g.z, g.N) && vec(g.residual, g.N), only_if, only_if_n);
 }
 
+// 128 x 128 tiles reuse each loaded element twice as often as 64 x 64 ones, which run where the large tiles would
+// leave SMs without one; up to 16 rows of A, tiles of 16.  S: blocks that share a tile.
+struct Tiling {
+    int rows, S;
+    int64_t tiles;
+};
+Tiling tiling(int64_t M, int64_t N, int64_t K, int sms) {
+    auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    if (M > 16 && tiles(128, 128) >= sms) return Tiling{128, 1, tiles(128, 128)};
+    Tiling t{M > 16 ? 64 : 16, 1, M > 16 ? tiles(64, 64) : tiles(16, 128)};
+    while (t.S < 8 && t.tiles * t.S * 2 <= 4 * sms && K >= 128 * t.S) t.S *= 2;      // up to four blocks per SM, 64 of K each
+    return t;
+}
+
 template <typename T, bool A_MN, bool B_MN>
 cudaError_t pick(const GemmArgs& g, const int* only_if, int only_if_n) {
     DeviceInfo di;
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
-    auto tiles = [&](int bm, int bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
     if constexpr (sizeof(T) == 4) {
         if (only_if) return launch<T, 128, 128, 8, 8, A_MN, B_MN, true>(g, 1, only_if, only_if_n);
     }
-    // 128 x 128 tiles reuse each loaded element twice as often as 64 x 64 ones, which run where the
-    // large tiles would leave SMs without one; up to 16 rows of A, tiles of 16
-    if (g.M > 16 && tiles(128, 128) >= di.sm_count)
-        return launch<T, 128, 128, 8, 8, A_MN, B_MN, false>(g, 1, nullptr, 0);
-    const int64_t n = g.M > 16 ? tiles(64, 64) : tiles(16, 128);
-    int S = 1;                                         // up to four blocks per SM, 64 of K each
-    while (S < 8 && n * S * 2 <= 4 * di.sm_count && g.K >= 128 * S) S *= 2;
-    return g.M > 16 ? launch<T, 64, 64, 4, 4, A_MN, B_MN, false>(g, S, nullptr, 0)
-                    : launch<T, 16, 128, 2, 4, A_MN, B_MN, false>(g, S, nullptr, 0);
+    const Tiling t = tiling(g.M, g.N, g.K, di.sm_count);
+    if (t.rows == 128) return launch<T, 128, 128, 8, 8, A_MN, B_MN, false>(g, 1, nullptr, 0);
+    return t.rows == 64 ? launch<T, 64, 64, 4, 4, A_MN, B_MN, false>(g, t.S, nullptr, 0)
+                        : launch<T, 16, 128, 2, 4, A_MN, B_MN, false>(g, t.S, nullptr, 0);
 }
 
 template <typename T>
@@ -267,6 +275,16 @@ cudaError_t pick_layout(const GemmArgs& g, const int* o, int n) {
 }
 
 }  // namespace
+
+// Measured over T = 9 to 2048, K and N = 256 to 4096, all three layouts (operands in L2): a step of 16 of K takes
+// longer the more blocks an SM has.  Off by a seventh (rms).  148 SMs whatever the device: the workspace's size
+// follows from it.
+double gemm_generic_time(int64_t M, int64_t N, int64_t K) {
+    const Tiling t = tiling(M, N, K, 148);
+    const double steps = (double)(((K + BK - 1) / BK + t.S - 1) / t.S), more = (double)((t.tiles * t.S + 147) / 148 - 1);
+    if (t.rows == 16) return 3.7 + steps * (0.63 + 0.77 * more);
+    return t.rows == 64 ? 3.2 + steps * (1.2 + 0.45 * more) : 7.0 + steps * (1.15 + 2.2 * more);
+}
 
 cudaError_t launch_gemm_generic(const GemmArgs& g, const int* only_if, int only_if_n) {
     return g.dt == BF16 ? pick_layout<__nv_bfloat16>(g, only_if, only_if_n) : pick_layout<float>(g, only_if, only_if_n);
