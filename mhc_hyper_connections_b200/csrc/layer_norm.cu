@@ -112,9 +112,11 @@ __device__ __forceinline__ void centre(float& mean, float& s, float t, int d) {
     mean += m1;
     s = fmaxf(fmaf(-t, m1, s), 0.f);
 }
-// Such a row in the kernels that hold many registers per thread: the walk over memory, not inlined, so that the
-// loop around it keeps its registers (T = 8192, d = 8192, fp32: 83 us, 96 with a walk over registers).  nthr
-// threads share the row, VEC elements at a time, G as in group_sum (buf: 32 floats for G = 0).
+// Such a row in most kernels that hold many registers per thread: the walk over memory, not inlined, so that
+// the loop around it keeps its registers (T = 8192, d = 8192, fp32: 83 us, 96 with a walk over registers).  Two
+// of them are better off with the walk over registers: bf16, T = 1000, d = 12288 19 us against 26 (the call
+// leaves 56 registers there), and odd d = 3453 9.8 against 12.3.  nthr threads share the row, VEC elements at a
+// time, G as in group_sum (buf: 32 floats for G = 0).
 template <typename T, int VEC, int G>
 __device__ __noinline__ float2 recentre(const T* __restrict__ row, int d, int idx, int nthr, float mean, float s,
                                         float* buf) {
@@ -162,8 +164,8 @@ ln_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
                               int64_t Tn, int d, float eps, T* __restrict__ y, float* __restrict__ mean_out,
                               float* __restrict__ rstd_out) {
     using P = Pack<T, VEC>;
-    __shared__ float buf[WARP ? 1 : 64 * R], far[WARP ? 1 : 32];
-    int phase = 0;
+    __shared__ float buf[WARP ? 1 : 64 * R], far[WARP ? 1 : 64];
+    int phase = 0, far_phase = 0;
     pdl_launch_next();
     pdl_wait();
     const int nthr = WARP ? 32 : blockDim.x;
@@ -227,14 +229,17 @@ ln_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w, const float*
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (!off_centre(mean[r], s[r], inv_d)) continue;      // the same in the whole group; rows past Tn are 0
-            if constexpr (NV == 1) {
-                float t[1] = {0.f}, f[VEC];
-                P::unpack(raw[r][0], f);
+            if constexpr (NV == 1 || (NV == 8 && !WARP && sizeof(T) == 2)) {
+                float t[1] = {0.f};
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (idx * VEC < d) t[0] += f[e] - mean[r];
-                static_assert(R == 1, "buf has room for R values");
-                group_sum<1, WARP ? 32 : 0>(t, buf, phase, nthr);
+                for (int v = 0; v < NV; ++v) {
+                    float f[VEC];
+                    P::unpack(raw[r][v], f);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if ((v * nthr + idx) * VEC < d) t[0] += f[e] - mean[r];
+                }
+                group_sum<1, WARP ? 32 : 0>(t, far, far_phase, nthr);
                 centre(mean[r], s[r], t[0], d);
             } else {
                 const float2 m = recentre<T, VEC, WARP ? 32 : 0>(x + (row0 + r * groups) * d, d, idx, nthr, mean[r],
@@ -591,9 +596,9 @@ __device__ __forceinline__ void load_columns(const float* __restrict__ p, int d,
 
 // Rows belong to groups of G lanes (G = 8, 16, 32), or to the block (G = 0).  A group takes R rows at
 // a time, NV 16-byte vectors per thread and row; a slot holds the B rows that the block takes at a time.
-// TH: the most threads that share a row and its registers.
+// TH: the most threads that share a row and its registers; 224 leaves room for a second block on the SM.
 template <typename T, int NV, int R, int G, int TH>
-__global__ void __launch_bounds__(TH + 32)
+__global__ void __launch_bounds__(TH + 32, TH == 224 ? 2 : 0)
 ln_fwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b, int64_t Tn, int d,
                    float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int slots,
                    Limits lim) {
@@ -663,11 +668,11 @@ ln_fwd_ring_kernel(const T* __restrict__ x, const float* __restrict__ w, const f
             s[r] = acc.x + acc.y;
         }
         group_sum<R, G>(s, buf, phase, nthr);
-        if constexpr (G != 0) {
-            bool off = false;
+        if constexpr (G != 0 || TH == 512) {
+            bool off = false;             // the same in the whole group
 #pragma unroll
             for (int r = 0; r < R; ++r) off |= off_centre(mean[r], s[r], inv_d);
-            if (__any_sync(0xffffffffu, off)) {
+            if (G ? __any_sync(0xffffffffu, off) : off) {
                 float t[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -1738,10 +1743,12 @@ cudaError_t bwd_shift(const LnArgs& a, int* blocks) {
 // The layout of a row by its length in vectors: 8, 16 or 32 lanes with one vector each, 32 with two, a
 // warp with up to 16, a block with more.  What a block's row costs is the time between its load and its
 // store, which other warps have to cover: several small blocks per SM, or one of ten warps and more whose
-// threads hold few registers each.  Measured, us: bf16, T = 8192, d = 6000, 4 vectors per thread and one row
-// 53 (2 and two rows: 59; 6: 53), d = 8192, 4 and two rows 66 (2 and two: 70, 4 and one: 76); fp32, T = 8192,
-// d = 7400, 6 and two rows 84 (4 and one: 107, 8 and one: 90), d = 5000, T = 5052, 8 and one 39 (42, 42).  At
-// most one row per SM takes a register kernel.
+// threads hold few registers each.  Measured, us, T = 8192, vectors per thread and rows at a time: bf16, d = 6000
+// 4 and one 49 (2 and two: 58; 4 and two: 61), d = 8192 4 and two 60 (2 and two: 69, 4 and one: 73); fp32, d =
+// 5000 8 and one 54 (6 and two: 66, 4 and one: 86), d = 7400 6 and two 80 (8 and one: 85, 4 and one: 98), d =
+// 3328 (T = 16384) 4 and two 81 (2 and two: 98).  Up to 224 threads two blocks fit if a thread holds 128 registers
+// at most (bf16, d = 6000: 76 with 136; fp32, T = 1000, d = 5376: 10.2 and 11.3).  At most one row per SM takes a
+// register kernel.
 // Rows that are not a multiple of 16 bytes take the shift kernels from 16 rows per SM on.  T = 16384,
 // bf16: d = 4095 forward 68 us against 132 one element at a time, backward 123 against 165; d = 2559
 // backward 86 against 104.  With fewer rows filling the ring costs more than it hides: T = 1200, d = 1037
@@ -1763,9 +1770,10 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
         if (c <= 320) return fwd_warp<T, 10>(a);
         if (c <= 384) return fwd_warp<T, 12>(a);
         if (c <= 512) return fwd_warp<T, 16>(a);
-        if (V == 8 && c <= 896) return fwd_ring<T, 4, 1, 0, 256>(a);
+        if (c <= 896) return fwd_ring<T, 4, V == 8 ? 1 : 2, 0, 224>(a);
         if (c <= 1024) return fwd_ring<T, 4, 2, 0, 256>(a);
         if (V == 4 && c <= 1280) return fwd_ring<T, 8, 1, 0, 256>(a);
+        if (V == 4 && c <= 1344) return fwd_ring<T, 6, 2, 0, 224>(a);
         if (V == 4 && c <= 2048) return fwd_ring<T, 6, 2, 0, 352>(a);
         if (c <= 2048) return fwd_ring<T, 4, 1, 0, 512>(a);
     } else {
