@@ -46,9 +46,11 @@ int bwd_blocks(int d) { return d >= 4096 ? 296 : d <= 1024 ? 1184 : 296 * 4096 /
 // kernel runs; above it from the row kernel's registers through `part`.  d = 2560, bf16, T = 128: 3.5 us
 // against 8.2, T = 500: 6.4 against 9.6, T = 1000: 14.4 against 11.5.
 constexpr int FEW_ROWS = 512;
-// Up to here both are one launch, where a block holds a row with one vector per thread: a call 9.7 us against
-// 12.1 (bound by the host; in a graph, bf16, T = 200, d = 1024: 3.6 against 3.7, T = 256, d = 4096: 5.9 and 6.6,
-// unaligned d = 515: 4.9 and 3.6).  Its column blocks have half the warps, so many rows take them longer.
+// Up to here both are one launch, where a block holds a row with one vector per thread: a call 9.5 us against
+// 11.7, bound by the host.  In a graph, where the device's time counts, it gains with fewer rows or longer ones
+// and loses with others (bf16, T = 64, d = 1024: 2.1 us against 3.6, T = 256, d = 4096: 5.9 and 6.6, fp32 7.6 and
+// 7.4; T = 128, d = 515: 2.9 and 2.7, both types; T = 256, d = 512 and 515: 4.9 and 3.5), because its column blocks
+// have half the warps.
 constexpr int ONE_LAUNCH_ROWS = 256;
 constexpr int WARPS = 8;               // warps per block where a row belongs to a warp
 
@@ -1750,9 +1752,9 @@ cudaError_t bwd_shift(const LnArgs& a, int* blocks) {
 // at most (bf16, d = 6000: 76 with 136; fp32, T = 1000, d = 5376: 10.2 and 11.3).  At most one row per SM takes a
 // register kernel.
 // Rows that are not a multiple of 16 bytes take the shift kernels from 16 rows per SM on.  T = 16384,
-// bf16: d = 4095 forward 68 us against 132 one element at a time, backward 123 against 165; d = 2559
-// backward 86 against 104.  With fewer rows filling the ring costs more than it hides: T = 1200, d = 1037
-// forward 7.4 against 5.8 us, T = 2400 7.9 against 9.4.
+// bf16: d = 4095 67 us against 137 one element at a time, d = 2559 49 against 89; fp32, d = 2559 71 against 76.
+// With fewer rows filling the ring costs more than it hides: T = 1200, d = 1037, bf16 7.4 against 6.1 us, T = 2400
+// 8.7 against 9.8.
 template <typename T>
 cudaError_t fwd_t(const LnArgs& a, int sms) {
     constexpr int V = Vec16<T>::VEC;
@@ -1815,10 +1817,14 @@ cudaError_t bwd_few(const LnArgs& a, bool aligned, bool* done) {
 }
 
 // As forward, but a block has two vectors per thread and two rows at a time up to 512 vectors, and three
-// (fp32, above 1024: six) and one above (T = 8192, bf16, d = 8192: 83 us, 142 with two; fp32 97, 172 with
-// four; odd widths, d = 6001: 101, 132 with two).  320 to 480 vectors: three and one, because two need six
-// warps or more, whose registers leave room for one block per SM only (T = 16384, bf16, d = 2816: 60 us
-// against 79, d = 3584: 71 against 80; d = 4096 needs six warps either way: 77 with two, 115 with three).
+// (fp32, above 1024: six) and one above.  Measured, us, x and dy apart: T = 8192, d = 8192, bf16 78 (142 with two
+// and one); fp32 140 (176 with four and one).  320 to 480 vectors: three and one, because two need six warps or
+// more, whose registers leave room for one block per SM only (T = 16384, bf16, d = 2816: 60 against 72, d = 3584:
+// 71 against 74; d = 4096 needs six warps either way: 77 with two and two, 109 with three and one).
+// Rows that are not a multiple of 16 bytes, T = 16384, against one element at a time: bf16, d = 2559 86 and 104,
+// d = 3585 101 and 157, d = 4609 two and two 138 (three and one: 175) and 283, d = 5633 three and one 173 and 302
+// (at T = 7101 83, two and two 112); fp32, d = 2305 four and one 85 (three and one: 133) and 109, d = 3585 147 and
+// 170.  With few rows the elements gain: T = 2400, bf16, d = 2559 24 and 20, d = 4609 30 and 38.
 template <typename T>
 cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
     constexpr int V = Vec16<T>::VEC;
@@ -1839,7 +1845,9 @@ cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
         const int c = ((int)sizeof(T) * a.d + 30) / 16;
         if (a.T >= 16 * sms && a.d > 256 && c <= 1024 && rows16(a.x) && rows16(a.dy) && rows16(a.dx)) {
             if (c > 320 && c <= 480) return bwd_shift<T, 3, 1, 256>(a, blocks);
-            if (c <= 512) return bwd_shift<T, 2, 2, 256>(a, blocks);
+            if (c <= (V == 8 ? 480 : 512)) return bwd_shift<T, 2, 2, 256>(a, blocks);
+            if (V == 8 && c <= 640) return bwd_shift<T, 2, 2, 320>(a, blocks);
+            if (V == 4 && c <= 640) return bwd_shift<T, 4, 1, 256>(a, blocks);
             return bwd_shift<T, 3, 1, 352>(a, blocks);
         }
         if (a.d <= 256) return bwd<T, 1, 8, 1, true>(a, blocks);
