@@ -316,7 +316,8 @@ mhc_status mhc_backward_noalloc(const void* X, const void* F_out, const float* p
  * Inputs : x [T,d] (dt); weight [d], bias [d] fp32, each may be NULL (1 and 0).
  * Outputs: y [T,d] (dt); mean [T], rstd [T] fp32, which the backward needs: both given or
  *          both NULL (MHC_ERR_NULL for one alone).
- * Statistics are fp32; the variance is summed around the mean.
+ * Statistics are fp32; the variance is summed around the mean.  A row of one value has that value as its
+ * mean, rstd = 1 / sqrt(eps) and y = bias.
  */
 mhc_status mhc_layer_norm(const void* x, const float* weight, const float* bias, int64_t T, int d,
                           float eps, mhc_dtype dt, void* y, float* mean, float* rstd,

@@ -1753,8 +1753,8 @@ cudaError_t bwd_shift(const LnArgs& a, int* blocks) {
 // register kernel.
 // Rows that are not a multiple of 16 bytes take the shift kernels from 16 rows per SM on.  T = 16384,
 // bf16: d = 4095 67 us against 137 one element at a time, d = 2559 49 against 89; fp32, d = 2559 71 against 76.
-// With fewer rows filling the ring costs more than it hides: T = 1200, d = 1037, bf16 7.4 against 6.1 us, T = 2400
-// 8.7 against 9.8.
+// With fewer rows filling the ring costs more than it hides: T = 1200, d = 1037, bf16 7.4 against 5.8 us, T = 2400
+// 7.9 against 9.4.
 template <typename T>
 cudaError_t fwd_t(const LnArgs& a, int sms) {
     constexpr int V = Vec16<T>::VEC;
