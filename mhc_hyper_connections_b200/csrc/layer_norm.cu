@@ -1774,10 +1774,13 @@ cudaError_t fwd_t(const LnArgs& a, int sms) {
         if (c <= 512) return fwd_warp<T, 16>(a);
         if (c <= 896) return fwd_ring<T, 4, V == 8 ? 1 : 2, 0, 224>(a);
         if (c <= 1024) return fwd_ring<T, 4, 2, 0, 256>(a);
-        if (V == 4 && c <= 1280) return fwd_ring<T, 8, 1, 0, 256>(a);
-        if (V == 4 && c <= 1344) return fwd_ring<T, 6, 2, 0, 224>(a);
-        if (V == 4 && c <= 2048) return fwd_ring<T, 6, 2, 0, 352>(a);
-        if (c <= 2048) return fwd_ring<T, 4, 1, 0, 512>(a);
+        if constexpr (V == 4) {
+            if (c <= 1280) return fwd_ring<T, 8, 1, 0, 256>(a);
+            if (c <= 1344) return fwd_ring<T, 6, 2, 0, 224>(a);
+            if (c <= 2048) return fwd_ring<T, 6, 2, 0, 352>(a);
+        } else {
+            if (c <= 2048) return fwd_ring<T, 4, 1, 0, 512>(a);
+        }
     } else {
         // vectors that the words around a row may take
         const int c = ((int)sizeof(T) * a.d + 30) / 16;
@@ -1846,8 +1849,11 @@ cudaError_t bwd_t(const LnArgs& a, int sms, int* blocks) {
         if (a.T >= 16 * sms && a.d > 256 && c <= 1024 && rows16(a.x) && rows16(a.dy) && rows16(a.dx)) {
             if (c > 320 && c <= 480) return bwd_shift<T, 3, 1, 256>(a, blocks);
             if (c <= (V == 8 ? 480 : 512)) return bwd_shift<T, 2, 2, 256>(a, blocks);
-            if (V == 8 && c <= 640) return bwd_shift<T, 2, 2, 320>(a, blocks);
-            if (V == 4 && c <= 640) return bwd_shift<T, 4, 1, 256>(a, blocks);
+            if constexpr (V == 8) {
+                if (c <= 640) return bwd_shift<T, 2, 2, 320>(a, blocks);
+            } else {
+                if (c <= 640) return bwd_shift<T, 4, 1, 256>(a, blocks);
+            }
             return bwd_shift<T, 3, 1, 352>(a, blocks);
         }
         if (a.d <= 256) return bwd<T, 1, 8, 1, true>(a, blocks);
