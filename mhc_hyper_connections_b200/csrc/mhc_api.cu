@@ -14,7 +14,9 @@ namespace mhc {
 
 static thread_local char g_last_error[256] = "";
 
+// The error is reported here and taken off the runtime's record, where the next call's launch check would find it.
 static mhc_status cuda_fail(cudaError_t e, const char* where) {
+    cudaGetLastError();
     snprintf(g_last_error, sizeof g_last_error, "%s: %s (%s)", where, cudaGetErrorName(e),
              cudaGetErrorString(e));
     return MHC_ERR_CUDA;
