@@ -421,7 +421,8 @@ mhc_status mhc_amax_gain(const float* H_layers, int L, int64_t T, int n, float* 
 /*
  * mhc_device_status -- read and clear the device-side status words of the tensor-core
  * kernels.  Their waits between warps and between the CTAs of a cluster are bounded in
- * time (1 s each); a wait that expires makes the kernel stop early, leaving its outputs
+ * time (1 s each; a product's wait for a whole sum has 4 us more per 64 of its length); a wait
+ * that expires makes the kernel stop early, leaving its outputs
  * incomplete, and sets a bit here naming the wait: bits 0-15 the cluster pre kernel, 16-23
  * the two-pass pre kernels, 24-28 the tensor-core dX / dphi step of mhc_backward, 29-31 the
  * sub-layer operators (29 their loads: the layer norms' and the products'; 30 and 31 the

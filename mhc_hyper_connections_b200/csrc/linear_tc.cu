@@ -57,6 +57,9 @@ constexpr int PAIR_THREADS = 32 * (2 + PAIR_EPI);
 // part of the workspace's size, so it does not follow the device; a smaller one takes more rounds.
 constexpr int PAIRS = 74;
 constexpr unsigned long long kWaitNs = 1000000000ull;    // 1 s per wait
+// more for a wait on a whole accumulator, per K block (0.3 us at most, measured): the sum over 2^31 tokens takes
+// 1.4 s, in which every stage comes in time
+constexpr unsigned long long kBlockNs = 4000ull;
 constexpr unsigned long long kDrainNs = 2000000000ull;   // 2 s for the drains at exit
 constexpr unsigned long long kLandNs = 2000000ull;       // after a failed wait: loads in flight land
 
@@ -71,6 +74,7 @@ __host__ __device__ constexpr uint32_t idesc(int mm, int nn, bool a_mn, bool b_m
 struct Waiter {
     volatile int* abort_flag;
     unsigned long long limit_ns;
+    __device__ __forceinline__ Waiter over(int blocks) const { return Waiter{abort_flag, limit_ns + blocks * kBlockNs}; }
     // true when the phase completed; false when the CTA is aborting or the wait expired
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, unsigned code,
                                                bool honour_abort = true) const {
@@ -582,7 +586,7 @@ gemm_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epil
             const Item it = item_at(i, work);
             const int64_t r0 = (int64_t)it.m * 256 + rank * 128 + 32 * q, c0 = (int64_t)it.n * BN + h * (BN / 4);
             if (it.block < 0) prefetch_residual(ep, r0, c0, BN / 4, M, N, lane);
-            if (!wait.warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC)) break;
+            if (!wait.over(it.k1 - it.k0).warp(accf(buf), (uint32_t)(tc >> 1) & 1u, E_ACC)) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < BN / 4; c += CW) {
@@ -962,7 +966,7 @@ gemm_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epi
             for (int c = 0; c < HALF; ++c)
                 if (n0 + h * HALF + c < Nc && r < Mr) res[c] = __ldg(ep.residual + (n0 + (int64_t)h * HALF + c) * Mr + r);
         }
-        done = wait.warp(accf, 0u, E_ACC);
+        done = wait.over(k_hi - k_lo).warp(accf, 0u, E_ACC);
         tc_fence_after();
     }
     if (S == 1) {
